@@ -16,7 +16,9 @@ keys j < k_len[b] only:
                        (sums over the sharing heads too; 0 for keys past k_len)
   checkpoint           groups of 32 elements share a power of two 2^e, the
                        smallest (e >= -127) with every |round(x / 2^e)| <= 127;
-                       element codes are those rounded quotients (half to even)
+                       element codes are those rounded quotients (half to even).
+                       e stops at 121, where codes saturate at 127, so that what
+                       a finite value loads as is finite
   checkpoint_backward  backward with q and o held as such codes
 """
 import math
@@ -299,9 +301,9 @@ def _plain_save(x):
     finite = torch.isfinite(amax)
     e = torch.frexp(torch.where(finite, amax, torch.zeros_like(amax)))[1] - 7
     e = torch.clamp(e, min=-127)
-    e = torch.where(amax * _pow2(-e) >= 127.5, e + 1, e)
+    e = torch.where(amax * _pow2(-e) >= 127.5, e + 1, e).clamp(max=121)
     e = torch.where(amax == 0, torch.full_like(e, -127), e)
-    codes = torch.round(torch.where(finite, g, torch.zeros_like(g)) * _pow2(-e))
+    codes = torch.round(torch.where(finite, g, torch.zeros_like(g)) * _pow2(-e)).clamp(-127, 127)
     exps = torch.where(finite, e + 127, torch.full_like(e, 255))
     return codes.to(torch.int8).reshape(B, H, N, d), exps.to(torch.uint8).squeeze(-1)
 
@@ -340,7 +342,8 @@ def exact(case, seed):
         for bit in (128, 64, 32, 16, 8, 4, 2, 1):   # the largest step that is too small, plus one
             more = e + bit
             e = torch.where(torch.round(top / _step64(more - 1)) > 127, more, e)
-        return (torch.round(x / _step64(e)) * _step64(e)).flatten(-2)
+        e = torch.clamp(e, max=121)
+        return (torch.clamp(torch.round(x / _step64(e)), -127, 127) * _step64(e)).flatten(-2)
     G = case["Hq"] // case["Hkv"]
     shape = (case["B"], case["Hq"], case["Nq"])
     kvshape = (case["B"], case["Hkv"], case["Nk"], case["d"])
