@@ -26,6 +26,8 @@ OP_KMEANS_ASSIGN = 6
 OP_ROUTE_TOPP = 7
 OP_CENTROIDS = 8
 MAX_CLUSTERS = 4096
+CROSS_FORWARD, CROSS_BACKWARD, CROSS_BACKWARD_CKPT = range(3)
+CHECKPOINT_GROUP = 32   # elements sharing one exponent
 
 EXPORTED = ("svgear_cluster", "svgear_kmeanspp_init", "svgear_kmeans_assign",
             "svgear_label_sort", "svgear_kmeans_update", "svgear_permute",
@@ -36,7 +38,10 @@ EXPORTED = ("svgear_cluster", "svgear_kmeanspp_init", "svgear_kmeans_assign",
             "svgear_route_topp", "svgear_key_variance", "svgear_attend_var",
             "svgear_probe_value_free", "svgear_diagnostics",
             "svgear_label_sort_noalloc", "svgear_selftest_wait", "svgear_layer",
-            "svgear_layer_host", "svgear_layer_workspace_bytes")
+            "svgear_layer_host", "svgear_layer_workspace_bytes",
+            "svgear_cross_workspace_bytes", "svgear_cross_attend",
+            "svgear_cross_attend_backward", "svgear_cross_attend_backward_ckpt",
+            "svgear_checkpoint_save", "svgear_checkpoint_load")
 
 
 class Dims(ctypes.Structure):
@@ -48,6 +53,17 @@ class LayerParams(ctypes.Structure):
     _fields_ = [("Cq", ctypes.c_int32), ("Ck", ctypes.c_int32), ("iters", ctypes.c_int32),
                 ("density", ctypes.c_float), ("topp", ctypes.c_float), ("scale", ctypes.c_float),
                 ("var_lambda", ctypes.c_float), ("seed", ctypes.c_uint64)]
+
+
+class Tokens(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64), ("stride_n", ctypes.c_int64)]
+
+
+class CrossDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("Nq", ctypes.c_int32), ("Nk", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
 
 
 class SvgearError(RuntimeError):
@@ -103,6 +119,14 @@ def lib():
         "svgear_layer_host": [P, P, P, Dims, ctypes.POINTER(LayerParams), P, P, P, P, P, P, SZ,
                               P],
         "svgear_layer_workspace_bytes": [Dims, ctypes.POINTER(LayerParams), I32],
+        "svgear_cross_workspace_bytes": [I32, CrossDims],
+        "svgear_cross_attend": [Tokens, Tokens, Tokens, CrossDims, P, F, Tokens, P, P, SZ, P],
+        "svgear_cross_attend_backward": [Tokens, Tokens, Tokens, Tokens, Tokens, P, CrossDims, P,
+                                         F, Tokens, Tokens, Tokens, P, SZ, P],
+        "svgear_cross_attend_backward_ckpt": [Tokens, P, P, Tokens, Tokens, P, P, P, CrossDims, P,
+                                              F, Tokens, Tokens, Tokens, P, SZ, P],
+        "svgear_checkpoint_save": [Tokens, Dims, P, P, P],
+        "svgear_checkpoint_load": [P, P, Dims, Tokens, P],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -110,6 +134,7 @@ def lib():
         f.restype = ctypes.c_int
     L.svgear_workspace_bytes.restype = SZ
     L.svgear_layer_workspace_bytes.restype = SZ
+    L.svgear_cross_workspace_bytes.restype = SZ
     L.svgear_status_string.restype = ctypes.c_char_p
     L.svgear_kernel_launches.restype = ctypes.c_uint64
     _L = L
@@ -563,3 +588,162 @@ def layer_host(Qh, Kh, Vh, Cq, Ck, iters, density, scale=None, seed=0, warm_q=No
         _ptr(Qh), _ptr(Kh), _ptr(Vh), dims, ctypes.byref(prm), _ptr(warm_q), _ptr(warm_k),
         _ptr(out), _ptr(cent_q), _ptr(cent_k), _ptr(ws), n, _stream()))
     return {"O_host": out, "cent_q": cent_q, "cent_k": cent_k}
+
+
+# ---------------------------------------------------------------------------
+# Dense cross attention and 8-bit activation checkpoints
+# ---------------------------------------------------------------------------
+@dataclass
+class Checkpoint:
+    """An activation [B, H, N, d] in 8 bits (svgear_checkpoint_save)."""
+    codes: torch.Tensor       # int8 [B, H, N, d]
+    exps: torch.Tensor        # uint8 [B, H, N, d // 32]
+    dtype: torch.dtype        # of the tensor it was saved from
+
+
+def _view(t, name, like=None, shape=None):
+    """A token tensor with strides as a Tokens struct.  like: a tensor whose
+    device and dtype it must have; shape: its required shape."""
+    if not (t.is_cuda and t.dim() == 4 and t.stride(-1) == 1):
+        raise ValueError("%s must be a CUDA tensor [B, H, N, d] with d contiguous" % name)
+    _dtype_code(t)
+    if like is not None and (t.device != like.device or t.dtype != like.dtype):
+        raise ValueError("%s must be a %s tensor on %s" % (name, like.dtype, like.device))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have the shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    return Tokens(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+
+
+def _dense(t, name, dtype, device, shape):
+    if not (t.device == device and t.is_contiguous() and t.dtype == dtype
+            and tuple(t.shape) == tuple(shape)):
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
+                         % (name, dtype, tuple(shape), device))
+    return t
+
+
+def _new_like(t):
+    """An uninitialised tensor of t's shape, type and, where t is dense, layout."""
+    out = torch.empty_like(t)
+    return out if out.stride(-1) == 1 else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _cross_dims(q_shape, K, V, k_len):
+    B, Hq, Nq, d = q_shape
+    Bk, Hkv, Nk, dk = K.shape
+    if Bk != B or dk != d:
+        raise ValueError("K must have the shape [%d, Hkv, Nk, %d], not %s" % (B, d, tuple(K.shape)))
+    if k_len is not None:
+        _dense(k_len, "k_len", torch.int32, K.device, (B,))
+    return CrossDims(B, Hq, Hkv, Nq, Nk, d, _dtype_code(K))
+
+
+def _cross_workspace(op, dims, device):
+    n = max(int(lib().svgear_cross_workspace_bytes(op, dims)), 256)
+    return torch.empty(n, dtype=torch.uint8, device=device), n
+
+
+def svgear_cross_attend(Q, K, V, scale=None, k_len=None, O=None, lse=None, check_status=False):
+    """Attention of Q [B, Hq, Nq, d] over an encoder's states K, V
+    [B, Hkv, Nk, d], Hkv dividing Hq, over the first k_len[b] keys (int32 [B];
+    default all; a batch with none gives 0 and lse -inf).  Tensors may be
+    strided with d contiguous.  Returns (O, lse): O of Q's type and layout,
+    lse float32 [B, Hq, Nq] for the backward pass.  scale defaults to
+    1 / sqrt(d)."""
+    q = _view(Q, "Q")
+    with torch.cuda.device(Q.device):
+        k, v = _view(K, "K", Q), _view(V, "V", Q, K.shape)
+        dims = _cross_dims(Q.shape, K, V, k_len)
+        O = _new_like(Q) if O is None else O
+        o = _view(O, "O", Q, Q.shape)
+        if lse is None:
+            lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device)
+        _dense(lse, "lse", torch.float32, Q.device, Q.shape[:3])
+        ws, n = _cross_workspace(CROSS_FORWARD, dims, Q.device)
+        _check("svgear_cross_attend", lib().svgear_cross_attend(
+            q, k, v, dims, _ptr(k_len), float(Q.shape[-1] ** -0.5 if scale is None else scale), o,
+            _ptr(lse), _ptr(ws), n, _stream()))
+        if check_status:
+            _device_status("svgear_cross_attend", ws, n)
+    return O, lse
+
+
+def svgear_cross_attend_backward(dO, Q, K, V, O, lse, scale=None, k_len=None, check_status=False):
+    """Gradients (dQ, dK, dV) of svgear_cross_attend's O, given its O and lse
+    and the gradient dO; each of its input's type and layout."""
+    q = _view(Q, "Q")
+    with torch.cuda.device(Q.device):
+        g, o = _view(dO, "dO", Q, Q.shape), _view(O, "O", Q, Q.shape)
+        k, v = _view(K, "K", Q), _view(V, "V", Q, K.shape)
+        dims = _cross_dims(Q.shape, K, V, k_len)
+        _dense(lse, "lse", torch.float32, Q.device, Q.shape[:3])
+        dQ, dK, dV = _new_like(Q), _new_like(K), _new_like(V)
+        ws, n = _cross_workspace(CROSS_BACKWARD, dims, Q.device)
+        _check("svgear_cross_attend_backward", lib().svgear_cross_attend_backward(
+            g, q, k, v, o, _ptr(lse), dims, _ptr(k_len),
+            float(Q.shape[-1] ** -0.5 if scale is None else scale), _view(dQ, "dQ"),
+            _view(dK, "dK"), _view(dV, "dV"), _ptr(ws), n, _stream()))
+        if check_status:
+            _device_status("svgear_cross_attend_backward", ws, n)
+    return dQ, dK, dV
+
+
+def svgear_checkpoint_save(X):
+    """X [B, H, N, d] (strided, d contiguous) in 8 bits: a Checkpoint."""
+    x = _view(X, "X")
+    B, H, N, d = X.shape
+    with torch.cuda.device(X.device):
+        codes = torch.empty(X.shape, dtype=torch.int8, device=X.device)
+        exps = torch.empty((B, H, N, d // CHECKPOINT_GROUP), dtype=torch.uint8, device=X.device)
+        _check("svgear_checkpoint_save", lib().svgear_checkpoint_save(
+            x, Dims(B, H, N, d, _dtype_code(X)), _ptr(codes), _ptr(exps), _stream()))
+    return Checkpoint(codes, exps, X.dtype)
+
+
+def _held(c, name, shape=None, device=None, dtype=None):
+    shape = c.codes.shape if shape is None else shape
+    device = c.codes.device if device is None else device
+    if not c.codes.is_cuda or c.codes.dim() != 4 or (dtype is not None and c.dtype != dtype):
+        raise ValueError("%s must be a Checkpoint of a CUDA %s tensor [B, H, N, d]"
+                         % (name, "token" if dtype is None else dtype))
+    _dense(c.codes, name + ".codes", torch.int8, device, shape)
+    _dense(c.exps, name + ".exps", torch.uint8, device,
+           tuple(shape[:3]) + (shape[3] // CHECKPOINT_GROUP,))
+    return _ptr(c.codes), _ptr(c.exps)
+
+
+def svgear_checkpoint_load(c, out=None):
+    """The tensor a Checkpoint stands for, in its type; dense unless `out`."""
+    codes, exps = _held(c, "c")
+    dev = c.codes.device
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty(c.codes.shape, dtype=c.dtype, device=dev)
+        x = _view(out, "out", shape=c.codes.shape)
+        if out.device != dev or out.dtype != c.dtype:
+            raise ValueError("out must be a %s tensor on %s" % (c.dtype, dev))
+        B, H, N, d = out.shape
+        _check("svgear_checkpoint_load", lib().svgear_checkpoint_load(
+            codes, exps, Dims(B, H, N, d, _dtype_code(out)), x, _stream()))
+    return out
+
+
+def svgear_cross_attend_backward_ckpt(dO, Qc, K, V, Oc, lse, scale=None, k_len=None,
+                                      check_status=False):
+    """svgear_cross_attend_backward with Q and O read from Checkpoints."""
+    g = _view(dO, "dO")
+    with torch.cuda.device(dO.device):
+        qc, qe = _held(Qc, "Qc", dO.shape, dO.device, dO.dtype)
+        oc, oe = _held(Oc, "Oc", dO.shape, dO.device, dO.dtype)
+        k, v = _view(K, "K", dO), _view(V, "V", dO, K.shape)
+        dims = _cross_dims(dO.shape, K, V, k_len)
+        _dense(lse, "lse", torch.float32, dO.device, dO.shape[:3])
+        dQ, dK, dV = _new_like(dO), _new_like(K), _new_like(V)
+        ws, n = _cross_workspace(CROSS_BACKWARD_CKPT, dims, dO.device)
+        _check("svgear_cross_attend_backward_ckpt", lib().svgear_cross_attend_backward_ckpt(
+            g, qc, qe, k, v, oc, oe, _ptr(lse), dims, _ptr(k_len),
+            float(dO.shape[-1] ** -0.5 if scale is None else scale), _view(dQ, "dQ"),
+            _view(dK, "dK"), _view(dV, "dV"), _ptr(ws), n, _stream()))
+        if check_status:
+            _device_status("svgear_cross_attend_backward_ckpt", ws, n)
+    return dQ, dK, dV

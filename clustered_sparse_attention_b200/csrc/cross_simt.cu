@@ -1,0 +1,590 @@
+// cross_simt.cu -- dense cross attention and its backward pass in fp32
+// arithmetic on the FMA pipe.
+//
+// Forward: s_ij = scale q_i.k_j over the keys j < k_len, an online softmax
+// (running maximum m, sum l), o_i = sum_j e^{s_ij - m} v_j / l and
+// lse_i = m + log l.  Backward: p_ij = e^{s_ij - lse_i},
+// ds_ij = p_ij (do_i.v_j - delta_i), dq_i = scale sum_j ds_ij k_j,
+// dk_j = scale sum_i ds_ij q_i, dv_j = sum_i p_ij do_i.
+//
+// 64 x 64 score tiles, 256 threads in a 16 x 16 grid, 4 x 4 scores and
+// 4 x D/16 outputs a thread: eight (S) or five (P V) shared-memory wavefronts
+// per 32 FMA instructions of a warp, so the FMA pipe is the bound.  Rows of
+// the shared tiles are D + 4 floats (16-byte units an odd number apart), so
+// the 16 column threads read 16 rows without a bank conflict.
+#include <math.h>
+
+#include "common.cuh"
+#include "cross.h"
+#include "launchers.h"
+
+namespace svgear {
+namespace {
+
+constexpr int M = kCrossSimtM, N = kCrossSimtN;
+constexpr int kThreads = 256;
+
+// rows [n0, n0 + 64) of head (b, h) as fp32 rows of D + 4, zeros from n_end on
+template <typename T, int D>
+__device__ __forceinline__ void load_tile(float* s, const svgear_tokens& t, int b, int h, int n0,
+                                          int n_end) {
+    constexpr int C = Elem<T>::kPerChunk, CH = D / C;
+    for (int i = threadIdx.x; i < 64 * CH; i += kThreads) {
+        const int r = i / CH, c = (i - r * CH) * C;
+        float v[C];
+        if (n0 + r < n_end) {
+            Elem<T>::load(row_ptr<const T>(t, b, h, n0 + r) + c, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < C; ++e) v[e] = 0.f;
+        }
+        float4* d4 = reinterpret_cast<float4*>(s + r * (D + 4) + c);
+#pragma unroll
+        for (int e = 0; e < C; e += 4) d4[e / 4] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+    }
+}
+
+// acc[i][j] = A[4 ty + i] . B[tx + 16 j]
+template <int D>
+__device__ __forceinline__ void dot_tile(const float* A, const float* Bm, int ty, int tx,
+                                         float (&acc)[4][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < D; k += 4) {
+        float4 a[4], c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * (D + 4) + k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[j] = *reinterpret_cast<const float4*>(Bm + (tx + 16 * j) * (D + 4) + k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[i][j] = fmaf(a[i].x, c[j].x, acc[i][j]);
+                acc[i][j] = fmaf(a[i].y, c[j].y, acc[i][j]);
+                acc[i][j] = fmaf(a[i].z, c[j].z, acc[i][j]);
+                acc[i][j] = fmaf(a[i].w, c[j].w, acc[i][j]);
+            }
+    }
+}
+
+// acc[i][4 c + e] += sum_n W[4 ty + i][n] X[n][64 c + 4 tx + e]; W rows of N + 4
+template <int D>
+__device__ __forceinline__ void accumulate(const float* W, const float* X, int ty, int tx,
+                                           float (&acc)[4][D / 16]) {
+#pragma unroll 2
+    for (int n = 0; n < N; n += 4) {
+        float4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(W + (4 * ty + i) * (N + 4) + n);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                const float4 x = *reinterpret_cast<const float4*>(X + (n + q) * (D + 4) + 64 * c + 4 * tx);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float wi = q == 0 ? w[i].x : q == 1 ? w[i].y : q == 2 ? w[i].z : w[i].w;
+                    acc[i][4 * c] = fmaf(wi, x.x, acc[i][4 * c]);
+                    acc[i][4 * c + 1] = fmaf(wi, x.y, acc[i][4 * c + 1]);
+                    acc[i][4 * c + 2] = fmaf(wi, x.z, acc[i][4 * c + 2]);
+                    acc[i][4 * c + 3] = fmaf(wi, x.w, acc[i][4 * c + 3]);
+                }
+            }
+        }
+    }
+}
+
+// acc[i][4 c + e] += sum_q W[q][4 ty + i] X[q][64 c + 4 tx + e] (W transposed)
+template <int D>
+__device__ __forceinline__ void accumulate_t(const float* W, const float* X, int ty, int tx,
+                                             float (&acc)[4][D / 16]) {
+#pragma unroll 4
+    for (int q = 0; q < M; ++q) {
+        const float4 w = *reinterpret_cast<const float4*>(W + q * (N + 4) + 4 * ty);
+        const float wi[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            const float4 x = *reinterpret_cast<const float4*>(X + q * (D + 4) + 64 * c + 4 * tx);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[i][4 * c] = fmaf(wi[i], x.x, acc[i][4 * c]);
+                acc[i][4 * c + 1] = fmaf(wi[i], x.y, acc[i][4 * c + 1]);
+                acc[i][4 * c + 2] = fmaf(wi[i], x.z, acc[i][4 * c + 2]);
+                acc[i][4 * c + 3] = fmaf(wi[i], x.w, acc[i][4 * c + 3]);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ float row_max16(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float row_sum16(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+    __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    uint2 u;
+    u.x = *reinterpret_cast<uint32_t*>(&a);
+    u.y = *reinterpret_cast<uint32_t*>(&b);
+    *reinterpret_cast<uint2*>(p) = u;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+cross_fwd_kernel(CrossArgs a, int splits, int tiles_per_split, float* __restrict__ o_part,
+                 float* __restrict__ lse_part) {
+    extern __shared__ float sm[];
+    float* sQ = sm;
+    float* sK = sQ + M * (D + 4);
+    float* sV = sK + N * (D + 4);
+    float* sP = sV + N * (D + 4);
+    const int qt = blockIdx.x / splits, sp = blockIdx.x - qt * splits;
+    const int b = blockIdx.y / a.Hq, h = blockIdx.y - b * a.Hq, hk = h / a.G;
+    const int q0 = qt * M, keys = cross_keys(a, b);
+    const int t0 = sp * tiles_per_split, t1 = min((keys + N - 1) / N, t0 + tiles_per_split);
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+
+    load_tile<T, D>(sQ, a.Q, b, h, q0, a.Nq);
+    float m[4], l[4], o[4][D / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
+    }
+    for (int t = t0; t < t1; ++t) {
+        __syncthreads();
+        load_tile<T, D>(sK, a.K, b, hk, t * N, keys);
+        load_tile<T, D>(sV, a.V, b, hk, t * N, keys);
+        __syncthreads();
+        float s[4][4];
+        dot_tile<D>(sQ, sK, ty, tx, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = t * N + tx + 16 * j < keys ? s[i][j] * a.scale : -INFINITY;
+                mx = fmaxf(mx, s[i][j]);
+            }
+            const float mn = fmaxf(m[i], row_max16(mx));
+            const float mu = mn == -INFINITY ? 0.f : mn;   // every score -inf so far
+            const float alpha = expf(m[i] - mu);
+            m[i] = mn;
+            l[i] *= alpha;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) o[i][c] *= alpha;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = expf(s[i][j] - mu);
+                l[i] += p;
+                sP[(4 * ty + i) * (N + 4) + tx + 16 * j] = p;
+            }
+        }
+        __syncthreads();
+        accumulate<D>(sP, sV, ty, tx, o);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float sum = row_sum16(l[i]);
+        const int row = q0 + 4 * ty + i;
+        if (row >= a.Nq) continue;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;   // no key: o = 0, lse = -inf
+        const float lse = sum == 0.f ? -INFINITY : m[i] + logf(sum);
+        const size_t r = (size_t)blockIdx.y * a.Nq + row;
+        if (splits > 1) {
+            const size_t rp = (size_t)sp * a.B * a.Hq * a.Nq + r;
+            if (tx == 0) lse_part[rp] = lse;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+                store4(o_part + rp * D + 64 * c + 4 * tx,
+                       make_float4(o[i][4 * c] * inv, o[i][4 * c + 1] * inv, o[i][4 * c + 2] * inv,
+                                   o[i][4 * c + 3] * inv));
+        } else {
+            if (tx == 0) a.lse[r] = lse;
+            T* dst = row_ptr<T>(a.O, b, h, row);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+                store4(dst + 64 * c + 4 * tx,
+                       make_float4(o[i][4 * c] * inv, o[i][4 * c + 1] * inv, o[i][4 * c + 2] * inv,
+                                   o[i][4 * c + 3] * inv));
+        }
+    }
+}
+
+// One warp per row: o = sum_s e^{lse_s - lse} o_s, lse = log sum_s e^{lse_s},
+// in split order.
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+cross_join_kernel(CrossArgs a, int splits, const float* __restrict__ o_part,
+                  const float* __restrict__ lse_part) {
+    const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
+    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (r >= rows) return;
+    const int lane = threadIdx.x & 31;
+    float mx = -INFINITY;
+    for (int s = 0; s < splits; ++s) mx = fmaxf(mx, lse_part[s * rows + r]);
+    const float mu = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f, o[D / 32];
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) o[c] = 0.f;
+    for (int s = 0; s < splits; ++s) {
+        const float ls = lse_part[s * rows + r];
+        if (ls == -INFINITY) continue;   // a split past the batch's keys
+        const float w = expf(ls - mu);
+        sum += w;
+        const float* p = o_part + (s * rows + r) * D;
+        if constexpr (D == 128) {
+            const float4 x = *reinterpret_cast<const float4*>(p + 4 * lane);
+            o[0] = fmaf(w, x.x, o[0]); o[1] = fmaf(w, x.y, o[1]);
+            o[2] = fmaf(w, x.z, o[2]); o[3] = fmaf(w, x.w, o[3]);
+        } else {
+            const float2 x = *reinterpret_cast<const float2*>(p + 2 * lane);
+            o[0] = fmaf(w, x.x, o[0]); o[1] = fmaf(w, x.y, o[1]);
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t bh = r / a.Nq;
+    const int b = (int)(bh / a.Hq), h = (int)(bh - (int64_t)b * a.Hq);
+    T* dst = row_ptr<T>(a.O, b, h, r - bh * a.Nq);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) dst[D / 32 * lane + c] = Elem<T>::to(o[c] * inv);
+    if (lane == 0) a.lse[r] = sum == 0.f ? -INFINITY : mx + logf(sum);
+}
+
+// ---------------------------------------------------------------------------
+// Backward
+// ---------------------------------------------------------------------------
+// p and ds of one 64 x 64 tile from its scores s and dp
+__device__ __forceinline__ void grad_tile(float (&s)[4][4], float (&dp)[4][4], const float* lse,
+                                          const float* delta, int ty, int tx, int k0, int keys,
+                                          float scale) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float p = k0 + tx + 16 * j < keys ? expf(s[i][j] * scale - lse[4 * ty + i]) : 0.f;
+            s[i][j] = p;
+            dp[i][j] = p == 0.f ? 0.f : p * (dp[i][j] - delta[4 * ty + i]);
+        }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) cross_dq_kernel(CrossArgs a) {
+    extern __shared__ float sm[];
+    float* sQ = sm;
+    float* sG = sQ + M * (D + 4);
+    float* sK = sG + M * (D + 4);
+    float* sV = sK + N * (D + 4);
+    float* sS = sV + N * (D + 4);
+    __shared__ float s_lse[M], s_delta[M];
+    const int b = blockIdx.y / a.Hq, h = blockIdx.y - b * a.Hq, hk = h / a.G;
+    const int q0 = blockIdx.x * M, keys = cross_keys(a, b);
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    load_tile<T, D>(sQ, a.Q, b, h, q0, a.Nq);
+    load_tile<T, D>(sG, a.dO, b, h, q0, a.Nq);
+    if (threadIdx.x < M) {
+        const int row = q0 + threadIdx.x;
+        const size_t r = (size_t)blockIdx.y * a.Nq + row;
+        s_lse[threadIdx.x] = row < a.Nq ? a.lse[r] : INFINITY;   // past the end: p = 0
+        s_delta[threadIdx.x] = row < a.Nq ? a.delta[r] : 0.f;
+    }
+    float dq[4][D / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) dq[i][c] = 0.f;
+    for (int t = 0; t * N < keys; ++t) {
+        __syncthreads();
+        load_tile<T, D>(sK, a.K, b, hk, t * N, keys);
+        load_tile<T, D>(sV, a.V, b, hk, t * N, keys);
+        __syncthreads();
+        float s[4][4], dp[4][4];
+        dot_tile<D>(sQ, sK, ty, tx, s);
+        dot_tile<D>(sG, sV, ty, tx, dp);
+        grad_tile(s, dp, s_lse, s_delta, ty, tx, t * N, keys, a.scale);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sS[(4 * ty + i) * (N + 4) + tx + 16 * j] = dp[i][j];
+        __syncthreads();
+        accumulate<D>(sS, sK, ty, tx, dq);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = q0 + 4 * ty + i;
+        if (row >= a.Nq) continue;
+        T* dst = row_ptr<T>(a.dQ, b, h, row);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+            store4(dst + 64 * c + 4 * tx,
+                   make_float4(dq[i][4 * c] * a.scale, dq[i][4 * c + 1] * a.scale,
+                               dq[i][4 * c + 2] * a.scale, dq[i][4 * c + 3] * a.scale));
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) cross_dkv_kernel(CrossArgs a, float* __restrict__ part) {
+    extern __shared__ float sm[];
+    float* sQ = sm;
+    float* sG = sQ + M * (D + 4);
+    float* sK = sG + M * (D + 4);
+    float* sV = sK + N * (D + 4);
+    float* sP = sV + N * (D + 4);
+    float* sS = sP + M * (N + 4);
+    __shared__ float s_lse[M], s_delta[M];
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const int qtiles = (a.Nq + M - 1) / M;
+    const int64_t per = (int64_t)a.G * qtiles;
+    const int64_t total = kv_total_units<N>(a) * per;
+    const int64_t end = kv_range(total, blockIdx.x + 1, gridDim.x);
+    KvCursor cur;
+    kv_cursor_start<N>(a, cur);
+    for (int64_t it = kv_range(total, blockIdx.x, gridDim.x); it < end;) {
+        const int64_t u = it / per;
+        const int64_t first = it - u * per, last = min(per, first + (end - it));
+        const KvUnit k = kv_unit<N>(a, cur, u);
+        __syncthreads();
+        load_tile<T, D>(sK, a.K, k.b, k.h, k.kt * N, k.keys);
+        load_tile<T, D>(sV, a.V, k.b, k.h, k.kt * N, k.keys);
+        float dk[4][D / 16], dv[4][D / 16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) dk[i][c] = dv[i][c] = 0.f;
+        for (int64_t x = first; x < last; ++x) {
+            const int g = (int)(x / qtiles), q0 = (int)(x - (int64_t)g * qtiles) * M;
+            const int h = k.h * a.G + g;
+            __syncthreads();
+            load_tile<T, D>(sQ, a.Q, k.b, h, q0, a.Nq);
+            load_tile<T, D>(sG, a.dO, k.b, h, q0, a.Nq);
+            if (threadIdx.x < M) {
+                const int row = q0 + threadIdx.x;
+                const size_t r = ((size_t)k.b * a.Hq + h) * a.Nq + row;
+                s_lse[threadIdx.x] = row < a.Nq ? a.lse[r] : INFINITY;
+                s_delta[threadIdx.x] = row < a.Nq ? a.delta[r] : 0.f;
+            }
+            __syncthreads();
+            float s[4][4], dp[4][4];
+            dot_tile<D>(sQ, sK, ty, tx, s);
+            dot_tile<D>(sG, sV, ty, tx, dp);
+            grad_tile(s, dp, s_lse, s_delta, ty, tx, k.kt * N, k.keys, a.scale);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    sP[(4 * ty + i) * (N + 4) + tx + 16 * j] = s[i][j];
+                    sS[(4 * ty + i) * (N + 4) + tx + 16 * j] = dp[i][j];
+                }
+            __syncthreads();
+            accumulate_t<D>(sP, sG, ty, tx, dv);
+            accumulate_t<D>(sS, sQ, ty, tx, dk);
+        }
+        const bool whole = first == 0 && last == per;
+        float* pk = part + ((size_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * 2 * N * D;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * ty + i, row = k.kt * N + r;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                const int col = 64 * c + 4 * tx;
+                const float4 vk = make_float4(dk[i][4 * c] * a.scale, dk[i][4 * c + 1] * a.scale,
+                                              dk[i][4 * c + 2] * a.scale, dk[i][4 * c + 3] * a.scale);
+                const float4 vv = make_float4(dv[i][4 * c], dv[i][4 * c + 1], dv[i][4 * c + 2],
+                                              dv[i][4 * c + 3]);
+                if (!whole) {
+                    store4(pk + r * D + col, vk);
+                    store4(pk + (N + r) * D + col, vv);
+                } else if (row < k.keys) {
+                    store4(row_ptr<T>(a.dK, k.b, k.h, row) + col, vk);
+                    store4(row_ptr<T>(a.dV, k.b, k.h, row) + col, vv);
+                }
+            }
+        }
+        it += last - first;
+    }
+}
+
+// Joins the partial sums of units cut between CTAs (in CTA order) and writes
+// zeros for the keys past k_len.  One CTA per (key tile, b * Hkv + h).
+template <typename T, int D, int BN>
+__global__ void __launch_bounds__(256)
+cross_dkv_join_kernel(CrossArgs a, int qrows, int ctas, const float* __restrict__ part) {
+    const int kt = blockIdx.x, b = blockIdx.y / a.Hkv, h = blockIdx.y - b * a.Hkv;
+    const int keys = cross_keys(a, b), nt = (keys + BN - 1) / BN;
+    const int64_t per = (int64_t)a.G * ((a.Nq + qrows - 1) / qrows);
+    int64_t before = 0;   // units of the batches before b
+    if (!a.k_len) {
+        before = (int64_t)b * a.Hkv * nt;
+    } else {
+        for (int x = threadIdx.x & 31; x < b; x += 32) before += (cross_keys(a, x) + BN - 1) / BN;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+        before *= a.Hkv;
+    }
+    const int64_t total = kv_total_units<BN>(a) * per;
+    int c0 = 0, c1 = -1;
+    if (kt < nt) {
+        const int64_t s = (before + (int64_t)h * nt + kt) * per, e = s + per;
+        // the CTAs whose ranges hold the unit's first and last iteration
+        int lo = 0, hi = ctas;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (kv_range(total, mid, ctas) <= s) lo = mid; else hi = mid;
+        }
+        c0 = lo;
+        lo = c0;
+        hi = ctas;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (kv_range(total, mid, ctas) < e) lo = mid; else hi = mid;
+        }
+        c1 = lo;
+    }
+    const int rows = min(BN, a.Nk - kt * BN);
+    const bool direct = kt < nt && c0 == c1;   // written by its CTA, but for the rows past k_len
+    for (int i = threadIdx.x; i < 2 * rows * (D / 4); i += blockDim.x) {
+        const int which = i / (rows * (D / 4)), rem = i - which * rows * (D / 4);
+        const int r = rem / (D / 4), col = (rem - r * (D / 4)) * 4, row = kt * BN + r;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < keys) {
+            if (direct) continue;
+            for (int c = c0; c <= c1; ++c) {
+                if (kv_range(total, c, ctas) == kv_range(total, c + 1, ctas)) continue;
+                const float4 x = *reinterpret_cast<const float4*>(
+                    part + (((size_t)c * 2 + (c == c0 ? 1 : 0)) * 2 + which) * BN * D + (size_t)r * D + col);
+                v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+            }
+        }
+        store4(row_ptr<T>(which ? a.dV : a.dK, b, h, row) + col, v);
+    }
+}
+
+// delta_i = do_i . o_i, one warp per row in fp32; o from its tensor or from
+// 8-bit codes, and with codes also q unpacked into qx [B][Hq][Nq][D].
+template <typename T, int D, bool HELD>
+__global__ void __launch_bounds__(256)
+cross_delta_kernel(CrossArgs a, HeldTokens qh, HeldTokens oh, T* __restrict__ qx) {
+    const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
+    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (r >= rows) return;
+    const int lane = threadIdx.x & 31;
+    constexpr int E = D / 32;   // elements per lane
+    const int64_t bh = r / a.Nq;
+    const int b = (int)(bh / a.Hq), h = (int)(bh - (int64_t)b * a.Hq);
+    const int64_t n = r - bh * a.Nq;
+    const T* g = row_ptr<const T>(a.dO, b, h, n) + E * lane;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        float o;
+        if (HELD) {
+            const int64_t i = r * D + E * lane + e;
+            o = (float)oh.codes[i] * held_step(oh.exps[i / 32]);
+            qx[i] = Elem<T>::to((float)qh.codes[i] * held_step(qh.exps[i / 32]));
+        } else {
+            o = Elem<T>::from(row_ptr<const T>(a.O, b, h, n)[E * lane + e]);
+        }
+        s = fmaf(Elem<T>::from(g[e]), o, s);
+    }
+    s = warp_sum(s);
+    if (lane == 0) a.delta[r] = s;
+}
+
+template <typename F>
+int set_smem(F* fn, size_t bytes) {
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess
+               ? SVGEAR_OK
+               : SVGEAR_ERR_CUDA;
+}
+
+template <typename T, int D>
+int fwd(const CrossArgs& a, CrossSplit sp, float* o_part, float* lse_part, cudaStream_t st) {
+    const size_t smem = sizeof(float) * (3 * 64 * (D + 4) + M * (N + 4));
+    if (int s = set_smem(cross_fwd_kernel<T, D>, smem)) return s;
+    cross_fwd_kernel<T, D><<<dim3((unsigned)ceil_div(a.Nq, M) * sp.splits, a.B * a.Hq), kThreads, smem, st>>>(
+        a, sp.splits, sp.tiles, o_part, lse_part);
+    count_launches(1);
+    SVGEAR_LAUNCH_CHECK();
+    return SVGEAR_OK;
+}
+template <typename T, int D>
+int join(const CrossArgs& a, int splits, const float* o_part, const float* lse_part, cudaStream_t st) {
+    const long long rows = (long long)a.B * a.Hq * a.Nq;
+    cross_join_kernel<T, D><<<ceil_div(rows, 8), 256, 0, st>>>(a, splits, o_part, lse_part);
+    count_launches(1);
+    SVGEAR_LAUNCH_CHECK();
+    return SVGEAR_OK;
+}
+template <typename T, int D>
+int delta(const CrossArgs& a, const HeldTokens* q, const HeldTokens* o, void* qx, cudaStream_t st) {
+    const int grid = ceil_div((long long)a.B * a.Hq * a.Nq, 8);
+    if (q)
+        cross_delta_kernel<T, D, true><<<grid, 256, 0, st>>>(a, *q, *o, static_cast<T*>(qx));
+    else
+        cross_delta_kernel<T, D, false><<<grid, 256, 0, st>>>(a, HeldTokens{}, HeldTokens{}, nullptr);
+    count_launches(1);
+    SVGEAR_LAUNCH_CHECK();
+    return SVGEAR_OK;
+}
+template <typename T, int D>
+int dq(const CrossArgs& a, cudaStream_t st) {
+    const size_t smem = sizeof(float) * (4 * 64 * (D + 4) + M * (N + 4));
+    if (int s = set_smem(cross_dq_kernel<T, D>, smem)) return s;
+    cross_dq_kernel<T, D><<<dim3(ceil_div(a.Nq, M), a.B * a.Hq), kThreads, smem, st>>>(a);
+    count_launches(1);
+    SVGEAR_LAUNCH_CHECK();
+    return SVGEAR_OK;
+}
+template <typename T, int D>
+int dkv(const CrossArgs& a, int ctas, float* part, cudaStream_t st) {
+    const size_t smem = sizeof(float) * (4 * 64 * (D + 4) + 2 * M * (N + 4));
+    if (int s = set_smem(cross_dkv_kernel<T, D>, smem)) return s;
+    cross_dkv_kernel<T, D><<<ctas, kThreads, smem, st>>>(a, part);
+    count_launches(1);
+    cross_dkv_join_kernel<T, D, N><<<dim3(ceil_div(a.Nk, N), a.B * a.Hkv), 256, 0, st>>>(a, M, ctas, part);
+    count_launches(1);
+    SVGEAR_LAUNCH_CHECK();
+    return SVGEAR_OK;
+}
+
+}  // namespace
+
+using bf16 = __nv_bfloat16;
+#define SVGEAR_PICK(f, ...)                                                             \
+    (dtype == SVGEAR_F32 ? (a.D == 128 ? f<float, 128>(__VA_ARGS__) : f<float, 64>(__VA_ARGS__)) \
+                         : (a.D == 128 ? f<bf16, 128>(__VA_ARGS__) : f<bf16, 64>(__VA_ARGS__)))
+
+int launch_cross_simt(const CrossArgs& a, int dtype, CrossSplit sp, float* o_part, float* lse_part,
+                      cudaStream_t st) {
+    return SVGEAR_PICK(fwd, a, sp, o_part, lse_part, st);
+}
+int launch_cross_join(const CrossArgs& a, int dtype, int splits, const float* o_part,
+                      const float* lse_part, cudaStream_t st) {
+    return SVGEAR_PICK(join, a, splits, o_part, lse_part, st);
+}
+int launch_cross_delta(const CrossArgs& a, int dtype, const HeldTokens* q, const HeldTokens* o,
+                       void* qx, cudaStream_t st) {
+    return SVGEAR_PICK(delta, a, q, o, qx, st);
+}
+int launch_cross_dq_simt(const CrossArgs& a, int dtype, cudaStream_t st) {
+    return SVGEAR_PICK(dq, a, st);
+}
+int launch_cross_dkv_simt(const CrossArgs& a, int dtype, int ctas, float* part, cudaStream_t st) {
+    return SVGEAR_PICK(dkv, a, ctas, part, st);
+}
+
+}  // namespace svgear

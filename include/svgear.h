@@ -535,6 +535,95 @@ int svgear_layer_host(const void* Q_host, const void* K_host, const void* V_host
                       const float* warm_k, void* O_host, float* cent_q, float* cent_k, void* ws,
                       size_t ws_bytes, void* stream);
 
+/* --------------------------------------------------------------------------
+ * Dense cross attention to an encoder's states, its gradients, and activation
+ * checkpoints in 8 bits: the dense operators a video block uses beside the
+ * clustered self-attention.
+ * ------------------------------------------------------------------------ */
+
+/* A token tensor [B][H][N][d] with element strides for its first three axes
+ * and d contiguous (so a projection's [B][N][H][d] output needs no copy).
+ * data and every stride in use are multiples of 16 bytes, strides are not
+ * negative and stride_n is not 0; the strides of an axis of length 1 are not
+ * used.  An input's stride_b and stride_h may be 0 (a broadcast tensor); the
+ * rows of an output must not overlap each other or an input. */
+typedef struct {
+    void* data;
+    int64_t stride_b, stride_h, stride_n;
+} svgear_tokens;
+
+/* Shapes of one call: Q, O and their gradients [B][Hq][Nq][d]; K, V and
+ * theirs [B][Hkv][Nk][d].  Hkv divides Hq: query head h reads key/value head
+ * h / (Hq / Hkv).  B, Hq >= 0 (0: nothing to do), Nq, Nk >= 1. */
+typedef struct {
+    int32_t B, Hq, Hkv, Nq, Nk, d;
+    int32_t dtype; /* svgear_dtype */
+} svgear_cross_dims;
+
+/* Operation selector for svgear_cross_workspace_bytes. */
+typedef enum {
+    SVGEAR_CROSS_FORWARD = 0,
+    SVGEAR_CROSS_BACKWARD = 1,
+    SVGEAR_CROSS_BACKWARD_CKPT = 2
+} svgear_cross_op;
+
+/* Workspace bytes of a cross attention call; 0 for arguments it would reject.
+ * The workspace starts with the device status words (svgear_device_status). */
+size_t svgear_cross_workspace_bytes(int32_t op, svgear_cross_dims dims);
+
+/* svgear_cross_attend -- softmax attention of every query over the keys
+ * j < k_len[b]:
+ *   s_ij = scale q_i.k_j, lse_i = log sum_j e^{s_ij},
+ *   O_i = sum_j e^{s_ij - lse_i} v_j.
+ *   k_len   int32[B] device, keys that take part (clamped to [0, Nk]), or NULL
+ *           for all.  What the rows of K and V past it hold does not matter.
+ *           With no key, O_i = 0 and lse_i = -inf.
+ *   scale   finite and > 0.
+ *   lse     out float[B][Hq][Nq], natural logarithm; the backward pass reads it.
+ * bf16 rounds the weights e^{s - m} (m: the running maximum) to bf16 for the
+ * product with V; sums and statistics are fp32. */
+int svgear_cross_attend(svgear_tokens Q, svgear_tokens K, svgear_tokens V, svgear_cross_dims dims,
+                        const int32_t* k_len, float scale, svgear_tokens O, float* lse, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/* svgear_cross_attend_backward -- gradients of svgear_cross_attend from the
+ * forward pass's O and lse:
+ *   p_ij = e^{s_ij - lse_i}, D_i = dO_i.O_i, ds_ij = p_ij (dO_i.v_j - D_i),
+ *   dQ_i = scale sum_j ds_ij k_j, dK_j = scale sum_i ds_ij q_i,
+ *   dV_j = sum_i p_ij dO_i, the sums over i also over the query heads that
+ * share the key/value head.  Rows of dK and dV past k_len, and dQ of a batch
+ * without keys, are 0.  A broadcast input gets the gradient of every one of
+ * its uses.  Every sum has a fixed order: equal calls give equal bits. */
+int svgear_cross_attend_backward(svgear_tokens dO, svgear_tokens Q, svgear_tokens K, svgear_tokens V,
+                                 svgear_tokens O, const float* lse, svgear_cross_dims dims,
+                                 const int32_t* k_len, float scale, svgear_tokens dQ,
+                                 svgear_tokens dK, svgear_tokens dV, void* ws, size_t ws_bytes,
+                                 void* stream);
+
+/* svgear_checkpoint_save / _load -- an activation held in 8 bits between the
+ * forward and the backward pass.  Groups of 32 consecutive elements of a row
+ * share 2^e, the smallest with e >= -127 for which every |round(x / 2^e)| is at
+ * most 127; codes are those quotients rounded half to even, exps e + 127.  e
+ * stops at 121, where codes saturate at 127: finite values load as finite.  A
+ * group with an infinity or NaN has exps 255 and loads as NaN.
+ *   codes  int8[B][H][N][d] (dense, 16-byte aligned), exps uint8[B][H][N][d/32].
+ * Loading gives codes * 2^e in dims.dtype (exact, but for bf16's rounding of
+ * results below its normal range). */
+int svgear_checkpoint_save(svgear_tokens X, svgear_dims dims, int8_t* codes, uint8_t* exps,
+                           void* stream);
+int svgear_checkpoint_load(const int8_t* codes, const uint8_t* exps, svgear_dims dims,
+                           svgear_tokens X, void* stream);
+
+/* svgear_cross_attend_backward_ckpt -- svgear_cross_attend_backward with Q and
+ * O read from checkpoints of shape [B][Hq][Nq][d]; the formulas are the same
+ * with the values the codes stand for. */
+int svgear_cross_attend_backward_ckpt(svgear_tokens dO, const int8_t* q_codes, const uint8_t* q_exps,
+                                      svgear_tokens K, svgear_tokens V, const int8_t* o_codes,
+                                      const uint8_t* o_exps, const float* lse,
+                                      svgear_cross_dims dims, const int32_t* k_len, float scale,
+                                      svgear_tokens dQ, svgear_tokens dK, svgear_tokens dV, void* ws,
+                                      size_t ws_bytes, void* stream);
+
 /* Workspace bytes for `op` at shape `dims` (N = tokens of the clustered
  * tensor; for SVGEAR_OP_ROUTE and SVGEAR_OP_ATTEND, dims.N = Nq and C2 = Ck),
  * with C1 = C (or Cq).  Returns 0 for arguments the op would reject. */

@@ -1,0 +1,167 @@
+"""Host-side checks of the cross attention and checkpoint entry points (no
+call below reaches the GPU), and of the tests' 64-bit forms against
+differences."""
+import ctypes
+
+import pytest
+import torch
+
+import cross_oracle as co
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from clustered_sparse_attention_b200 import build
+    build.build()
+    from clustered_sparse_attention_b200 import _lib
+    return _lib
+
+
+FAKE = 1 << 20      # never dereferenced: validation fails first
+BIG = ctypes.c_size_t(1 << 42)
+
+
+def _tok(m, N=100, H=4, d=128, data=FAKE, sb=None, sh=None, sn=None):
+    sn = d if sn is None else sn
+    sh = N * sn if sh is None else sh
+    return m.Tokens(data, H * sh if sb is None else sb, sh, sn)
+
+
+def _fwd(m, dims=None, Q=None, K=None, V=None, O=None, lse=FAKE, scale=0.1, ws=FAKE, n=BIG):
+    dims = m.CrossDims(2, 4, 4, 100, 100, 128, m.BF16) if dims is None else dims
+    t = _tok(m)
+    return m.lib().svgear_cross_attend(Q or t, K or t, V or t, dims, None, scale, O or t, lse, ws,
+                                       n, None)
+
+
+def test_forward_refusals(lib):
+    m = lib
+    bad, uns = m.ERR_INVALID_ARG, m.ERR_UNSUPPORTED
+    D = m.CrossDims
+    for dims, want in ((D(2, 4, 3, 100, 100, 128, 1), bad),      # Hkv does not divide Hq
+                       (D(2, 4, 0, 100, 100, 128, 1), bad),
+                       (D(2, 4, 4, 0, 100, 128, 1), bad),
+                       (D(2, 4, 4, 100, 0, 128, 1), bad),
+                       (D(-1, 4, 4, 100, 100, 128, 1), bad),
+                       (D(2, 4, 4, 100, 100, 96, 1), uns),
+                       (D(2, 4, 4, 100, 100, 128, 2), uns),
+                       (D(2, 40000, 40000, 100, 100, 128, 1), uns),
+                       (D(2, 1024, 1024, 1 << 20, 100, 128, 1), uns)):
+        assert _fwd(m, dims) == want
+        assert m.lib().svgear_cross_workspace_bytes(m.CROSS_FORWARD, dims) == 0
+    assert _fwd(m, Q=_tok(m, data=None)) == bad
+    assert _fwd(m, Q=_tok(m, data=FAKE + 8)) == bad              # alignment
+    assert _fwd(m, K=_tok(m, sn=132)) == bad                     # 264-byte rows
+    assert _fwd(m, V=_tok(m, sn=-128)) == bad
+    assert _fwd(m, V=_tok(m, sn=0)) == bad
+    assert _fwd(m, V=_tok(m, sh=1 << 40)) == bad
+    assert _fwd(m, O=_tok(m, sn=64)) == bad                      # rows overlap
+    assert _fwd(m, O=_tok(m, sh=0)) == bad                       # heads overlap
+    assert _fwd(m, O=_tok(m, sh=128, sn=256)) == bad             # 4 heads of 128 in 256
+    assert _fwd(m, lse=None) == bad
+    assert _fwd(m, ws=None) == bad
+    for scale in (0.0, -0.1, float("inf"), float("nan"), 3e38):
+        assert _fwd(m, scale=scale) == bad
+    assert _fwd(m, n=ctypes.c_size_t(64)) == m.ERR_WORKSPACE
+    assert m.lib().svgear_cross_workspace_bytes(9, D(2, 4, 4, 100, 100, 128, 1)) == 0
+
+
+def test_backward_refusals(lib):
+    m = lib
+    L, dims, t = m.lib(), m.CrossDims(2, 4, 4, 100, 100, 128, m.BF16), _tok(m)
+
+    def call(dims=dims, dO=t, dQ=t, dK=t, dV=t, O=t, lse=FAKE, scale=0.1, n=BIG):
+        return L.svgear_cross_attend_backward(dO, t, t, t, O, lse, dims, None, scale, dQ, dK, dV,
+                                              FAKE, n, None)
+
+    def held(qc=FAKE, qe=FAKE, oc=FAKE, oe=FAKE, n=BIG):
+        return L.svgear_cross_attend_backward_ckpt(t, qc, qe, t, t, oc, oe, FAKE, dims, None, 0.1, t,
+                                                   t, t, FAKE, n, None)
+
+    for kw in (dict(dO=_tok(m, data=None)), dict(dQ=_tok(m, sh=0)), dict(dK=_tok(m, sb=0)),
+               dict(dV=_tok(m, sn=64)), dict(O=_tok(m, data=FAKE + 2)), dict(lse=None),
+               dict(scale=0.0)):
+        assert call(**kw) == m.ERR_INVALID_ARG, kw
+    for kw in (dict(qc=None), dict(qe=None), dict(oc=None), dict(oe=None), dict(qc=FAKE + 8)):
+        assert held(**kw) == m.ERR_INVALID_ARG, kw
+    small = ctypes.c_size_t(L.svgear_cross_workspace_bytes(m.CROSS_BACKWARD, dims))
+    assert held(n=small) == m.ERR_WORKSPACE
+    assert call(n=ctypes.c_size_t(small.value - 1)) == m.ERR_WORKSPACE
+    assert call(dims=m.CrossDims(2, 4, 4, 100, 100, 80, m.BF16)) == m.ERR_UNSUPPORTED
+
+
+def test_checkpoint_refusals(lib):
+    m = lib
+    L, dims, t = m.lib(), m.Dims(2, 4, 100, 128, m.BF16), _tok(m)
+    assert L.svgear_checkpoint_save(t, dims, None, FAKE, None) == m.ERR_INVALID_ARG
+    assert L.svgear_checkpoint_save(t, dims, FAKE + 4, FAKE, None) == m.ERR_INVALID_ARG
+    assert L.svgear_checkpoint_save(_tok(m, sn=4), dims, FAKE, FAKE, None) == m.ERR_INVALID_ARG
+    assert L.svgear_checkpoint_load(FAKE, FAKE, dims, _tok(m, sn=64), None) == m.ERR_INVALID_ARG
+    assert L.svgear_checkpoint_load(FAKE, None, dims, t, None) == m.ERR_INVALID_ARG
+    assert L.svgear_checkpoint_save(t, m.Dims(2, 4, 100, 32, m.BF16), FAKE, FAKE,
+                                    None) == m.ERR_UNSUPPORTED
+    assert L.svgear_checkpoint_save(t, m.Dims(2, 4, 0, 128, m.BF16), FAKE, FAKE,
+                                    None) == m.ERR_INVALID_ARG
+
+
+def test_nothing_to_do(lib):
+    m = lib
+    t = _tok(m, data=None)
+    for dims in (m.CrossDims(0, 4, 4, 10, 10, 64, m.F32), m.CrossDims(2, 0, 0, 10, 10, 64, m.BF16)):
+        assert _fwd(m, dims, t, t, t, t, lse=None) == m.OK
+        assert m.lib().svgear_cross_attend_backward(t, t, t, t, t, None, dims, None, 0.1, t, t, t,
+                                                    FAKE, BIG, None) == m.OK
+    assert m.lib().svgear_checkpoint_save(t, m.Dims(0, 4, 10, 64, m.F32), None, None, None) == m.OK
+
+
+def test_binding_refuses_before_any_call():
+    import clustered_sparse_attention_b200 as csa
+    q = torch.zeros(1, 2, 4, 64)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        csa.svgear_cross_attend(q, q, q)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        csa.svgear_checkpoint_save(q)
+    with pytest.raises(ValueError, match="Checkpoint"):
+        csa.svgear_checkpoint_load(csa.Checkpoint(torch.zeros(1, 2, 4, 64, dtype=torch.int8),
+                                                  torch.zeros(1, 2, 4, 2, dtype=torch.uint8),
+                                                  torch.float32))
+
+
+def test_oracle_gradients_match_differences():
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn(2, 4, 3, 8, generator=g, dtype=torch.float64)
+    k, v = (torch.randn(2, 2, 5, 8, generator=g, dtype=torch.float64) for _ in range(2))
+    do = torch.randn(2, 4, 3, 8, generator=g, dtype=torch.float64)
+    k_len, scale = [5, 3], 0.4
+
+    def loss(q, k, v):
+        return float((co.forward(q, k, v, scale, k_len)[0] * do).sum())
+
+    o, lse, _, _ = co.forward(q, k, v, scale, k_len)
+    grads, _ = co.backward(do, q, k, v, o, lse, scale, k_len)
+    h = 1e-5
+    for i, t in enumerate((q, k, v)):
+        flat = t.view(-1)
+        for j in range(0, flat.numel(), 7):
+            x = float(flat[j])
+            flat[j] = x + h
+            up = loss(q, k, v)
+            flat[j] = x - h
+            down = loss(q, k, v)
+            flat[j] = x
+            # central difference: h^2 / 6 |f'''| (a few units here) + eps / h
+            assert abs((up - down) / (2 * h) - float(grads[i].view(-1)[j])) <= 1e-7
+
+
+def test_oracle_pack_rule():
+    x = torch.zeros(1, 1, 7, 32)
+    x[0, 0, 0, 0] = 1.0                          # 64 steps of 2^-6
+    x[0, 0, 1, 0] = 127.5 / 64                   # rounds to 128: one step up
+    x[0, 0, 2, 0] = 127.25 / 64
+    x[0, 0, 4, 3] = float("inf")
+    x[0, 0, 5] = 3e38
+    x[0, 0, 6] = -torch.finfo(torch.float32).max  # saturates
+    codes, exps = co.pack(x)
+    assert exps[0, 0, :, 0].tolist() == [121, 122, 121, 0, 255, 248, 248]
+    assert codes[0, 0, :, 0].tolist() == [64, 64, 127, 0, 0, 113, -127]
+    assert torch.isnan(co.unpack(codes, exps)[0, 0, 4]).all()
