@@ -107,8 +107,12 @@ CrossSplit cross_split(long long items, int key_tiles, int slots, int min_tiles)
 // persistent kernels are sized for them.
 constexpr int kSms = 148;
 
-int launch_cross_simt(const CrossArgs& a, int dtype, CrossSplit sp, float* o_part, float* lse_part,
-                      cudaStream_t st);
+int launch_cross_simt(const CrossArgs& a, CrossSplit sp, float* o_part, float* lse_part,
+                      cudaStream_t st);   // fp32
+// cross_sm100.cu (bf16): the partial results a call leaves (1: none), and the
+// call; err: device status words.
+int cross_sm100_parts(int B, int Hq, int Nq, int Nk);
+int launch_cross_sm100(const CrossArgs& a, float* o_part, float* lse_part, int* err, cudaStream_t st);
 int launch_cross_join(const CrossArgs& a, int dtype, int splits, const float* o_part,
                       const float* lse_part, cudaStream_t st);
 

@@ -92,16 +92,22 @@ size_t rows_of(const svgear_cross_dims& d) { return (size_t)d.B * d.Hq * d.Nq; }
 
 struct FwdWs {
     int* status;
-    float* o_part;     // [splits][B][Hq][Nq][d]
-    float* lse_part;   // [splits][B][Hq][Nq]
-    CrossSplit sp;
+    float* o_part;     // [parts][B][Hq][Nq][d], with more than one part
+    float* lse_part;   // [parts][B][Hq][Nq]
+    int parts;
+    CrossSplit sp;     // fp32
 };
 FwdWs carve_fwd(Carve& cv, const svgear_cross_dims& d) {
     FwdWs w;
-    const long long items = (long long)d.B * d.Hq * ceil_div(d.Nq, kCrossSimtM);
-    w.sp = cross_split(items, ceil_div(d.Nk, kCrossSimtN), kSms, kSimtMinTiles);
+    if (d.dtype == SVGEAR_BF16) {
+        w.parts = cross_sm100_parts(d.B, d.Hq, d.Nq, d.Nk);
+    } else {
+        const long long items = (long long)d.B * d.Hq * ceil_div(d.Nq, kCrossSimtM);
+        w.sp = cross_split(items, ceil_div(d.Nk, kCrossSimtN), kSms, kSimtMinTiles);
+        w.parts = w.sp.splits;
+    }
     w.status = cv.take<int>(4);
-    const size_t parts = w.sp.splits > 1 ? w.sp.splits * rows_of(d) : 0;
+    const size_t parts = w.parts > 1 ? w.parts * rows_of(d) : 0;
     w.o_part = cv.take<float>(parts * d.d);
     w.lse_part = cv.take<float>(parts);
     return w;
@@ -209,9 +215,11 @@ int svgear_cross_attend(svgear_tokens Q, svgear_tokens K, svgear_tokens V, svgea
     a.Q = Q; a.K = K; a.V = V; a.O = O;
     a.lse = lse;
     if (cudaMemsetAsync(w.status, 0, 4 * sizeof(int), st) != cudaSuccess) return SVGEAR_ERR_CUDA;
-    if ((s = launch_cross_simt(a, dims.dtype, w.sp, w.o_part, w.lse_part, st))) return s;
-    return w.sp.splits > 1 ? launch_cross_join(a, dims.dtype, w.sp.splits, w.o_part, w.lse_part, st)
-                           : SVGEAR_OK;
+    s = dims.dtype == SVGEAR_BF16 ? launch_cross_sm100(a, w.o_part, w.lse_part, w.status, st)
+                                  : launch_cross_simt(a, w.sp, w.o_part, w.lse_part, st);
+    if (s) return s;
+    return w.parts > 1 ? launch_cross_join(a, dims.dtype, w.parts, w.o_part, w.lse_part, st)
+                       : SVGEAR_OK;
 }
 
 int svgear_cross_attend_backward(svgear_tokens dO, svgear_tokens Q, svgear_tokens K, svgear_tokens V,

@@ -568,9 +568,10 @@ using bf16 = __nv_bfloat16;
     (dtype == SVGEAR_F32 ? (a.D == 128 ? f<float, 128>(__VA_ARGS__) : f<float, 64>(__VA_ARGS__)) \
                          : (a.D == 128 ? f<bf16, 128>(__VA_ARGS__) : f<bf16, 64>(__VA_ARGS__)))
 
-int launch_cross_simt(const CrossArgs& a, int dtype, CrossSplit sp, float* o_part, float* lse_part,
+int launch_cross_simt(const CrossArgs& a, CrossSplit sp, float* o_part, float* lse_part,
                       cudaStream_t st) {
-    return SVGEAR_PICK(fwd, a, sp, o_part, lse_part, st);
+    return a.D == 128 ? fwd<float, 128>(a, sp, o_part, lse_part, st)
+                      : fwd<float, 64>(a, sp, o_part, lse_part, st);
 }
 int launch_cross_join(const CrossArgs& a, int dtype, int splits, const float* o_part,
                       const float* lse_part, cudaStream_t st) {

@@ -1,0 +1,147 @@
+// cross_tc.cuh -- what the tcgen05 kernels of the cross attention share:
+// tensor maps of strided token views and the copy of a key tile whose rows
+// past the batch's key count must read as zeros.
+#pragma once
+
+#include "common.cuh"
+#include "cross.h"
+#include "tc_ptx.cuh"
+#include "tc_wait.cuh"
+#include "tma_host.h"
+
+namespace svgear {
+namespace crosstc {
+
+constexpr int BM = 128;   // query rows per tile
+constexpr int BN = 128;   // keys per tile
+
+// One token tensor: boxes of 2^i rows (i = 0..7; a whole tile is [7]) and
+// whether its head and batch axes move (a broadcast axis stays at 0).
+struct RowMaps {
+    CUtensorMap box[8];
+    int hmul, bmul;
+};
+struct TileMap {
+    CUtensorMap box;
+    int hmul, bmul;
+};
+
+inline bool make_row_maps(RowMaps* m, const svgear_tokens& t, int B, int H, int N, int D) {
+    m->hmul = t.stride_h != 0;
+    m->bmul = t.stride_b != 0;
+    for (int i = 0; i < 8; ++i)
+        if (!make_tokens_map(&m->box[i], t, B, H, N, D, 1u << i)) return false;
+    return true;
+}
+inline bool make_tile_map(TileMap* m, const svgear_tokens& t, int B, int H, int N, int D) {
+    m->hmul = t.stride_h != 0;
+    m->bmul = t.stride_b != 0;
+    return make_tokens_map(&m->box, t, B, H, N, D, BM);
+}
+
+// Copies a 128-row tile from row n0 of head (b, h) into shared memory (D / 64
+// regions of 128 rows x 128 bytes); rows past the tensor read as zeros.
+template <int D>
+__device__ __forceinline__ void load_tile(const TileMap& m, uint32_t dst, int b, int h, int n0,
+                                          uint32_t bar) {
+    tc::mbar_arrive_expect_tx(bar, BM * D * 2);
+#pragma unroll
+    for (int g = 0; g < D / 64; ++g)
+        tc::tma_load_4d(dst + g * 16384, &m.box, g * 64, n0, h * m.hmul, b * m.bmul, bar);
+}
+
+// As load_tile, with rows past `keys` (the batch's key count) reading as
+// zeros: they may hold anything, and 0 * NaN would spoil a product.  Where
+// the tile ends inside the tensor but past the keys, its valid rows are
+// covered by at most two boxes of 2^k rows (one at the start, one ending at
+// the end; where they overlap both write the same bytes) and the rest by
+// boxes that start past the tensor.
+template <int D>
+__device__ __forceinline__ void load_key_tile(const RowMaps& m, uint32_t dst, int b, int h, int n0,
+                                              int keys, int N, uint32_t bar) {
+    const int hc = h * m.hmul, bc = b * m.bmul;
+    const int n = keys - n0;
+    if (n >= BN || keys == N) {
+        tc::mbar_arrive_expect_tx(bar, BN * D * 2);
+#pragma unroll
+        for (int g = 0; g < D / 64; ++g)
+            tc::tma_load_4d(dst + g * 16384, &m.box[7], g * 64, n0, hc, bc, bar);
+        return;
+    }
+    const int k0 = 31 - __clz(n), k1 = 31 - __clz(BN - n);
+    const uint32_t rows = (uint32_t)((1 << k0) * (n == (1 << k0) ? 1 : 2) +
+                                     (1 << k1) * (BN - n == (1 << k1) ? 1 : 2));
+    tc::mbar_arrive_expect_tx(bar, rows * D * 2);
+#pragma unroll 1
+    for (int g = 0; g < D / 64; ++g) {
+        const uint32_t t = dst + g * 16384;
+        tc::tma_load_4d(t, &m.box[k0], g * 64, n0, hc, bc, bar);
+        if (n != (1 << k0))
+            tc::tma_load_4d(t + (n - (1 << k0)) * 128, &m.box[k0], g * 64, n0 + n - (1 << k0), hc, bc, bar);
+        tc::tma_load_4d(t + n * 128, &m.box[k1], g * 64, N, hc, bc, bar);
+        if (BN - n != (1 << k1))
+            tc::tma_load_4d(t + (BN - (1 << k1)) * 128, &m.box[k1], g * 64, N, hc, bc, bar);
+    }
+}
+
+// S (128 x 128) = A B^T over D, both K-major tiles in shared memory.
+template <int D>
+__device__ __forceinline__ void mma_dot(uint32_t d_tmem, uint32_t sA, uint32_t sB) {
+    constexpr uint32_t kIdesc = tc::idesc_bf16(BM, BN, false);
+    if constexpr (D == 128) {
+        tc::mma_bf16_k128(d_tmem, tc::sw128_desc(sA, 16, 1024), tc::sw128_desc(sB, 16, 1024), kIdesc, 0u);
+    } else {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+            tc::mma_bf16(d_tmem, tc::sw128_desc(sA + ks * 32, 16, 1024),
+                         tc::sw128_desc(sB + ks * 32, 16, 1024), kIdesc, ks > 0);
+    }
+}
+// O (128 x D) (+)= P X: P (128 x 128 bf16) in tensor memory, X a row tile in
+// shared memory read MN-major.
+template <int D>
+__device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a_tmem, uint32_t sX,
+                                         uint32_t accumulate) {
+    tc::mma_bf16_ts_k128(d_tmem, a_tmem, tc::sw128_desc(sX, 16384, 1024), tc::idesc_bf16(BM, D, true),
+                         accumulate);
+}
+
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
+}
+// (o0, o1) = (x0, x1) * m + a on packed fp32 pairs
+__device__ __forceinline__ void fma2(uint32_t x0, uint32_t x1, uint64_t m, uint64_t a, uint32_t& o0,
+                                     uint32_t& o1) {
+    asm("{\n\t.reg .b64 x, r;\n\tmov.b64 x, {%2, %3};\n\t"
+        "fma.rn.f32x2 r, x, %4, %5;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=r"(o0), "=r"(o1) : "r"(x0), "r"(x1), "l"(m), "l"(a));
+}
+// s += (p0, p1) on a packed fp32 pair
+__device__ __forceinline__ void add2(uint64_t& s, float p0, float p1) {
+    asm("{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\tadd.rn.f32x2 %0, %0, x;\n\t}"
+        : "+l"(s) : "f"(p0), "f"(p1));
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A slot ring's position: slot index and the parity of its current use.
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++slot == n) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+}  // namespace crosstc
+}  // namespace svgear

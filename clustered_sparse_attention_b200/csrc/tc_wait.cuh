@@ -49,6 +49,18 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
     }
 }
 
+// As wait_bar for copies or MMAs already issued, while a kernel gives up: it
+// ignores the abort flags and only the clock ends it.
+__device__ __forceinline__ bool drain_bar(uint64_t* bar, uint32_t parity) {
+    const uint32_t b = smem_u32(bar);
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 0; it < kMaxSpins; ++it) {
+        if (mbar_try_wait(b, parity)) return true;
+        if ((it & 63) == 63 && global_timer_ns() - t0 > kWaitTimeoutNs) return false;
+    }
+    return false;
+}
+
 // The device's tensor-memory-lost word (guard.cu): set by a kernel that kept
 // its TMEM columns because an MMA it issued may still have been running.
 __device__ __forceinline__ void mark_tmem_lost(int* lost) {
