@@ -36,8 +36,8 @@ namespace crosstc {
 namespace {
 
 using bf16 = __nv_bfloat16;
-using tc::wait_bar;
-using tc::warp_wait_bar;
+using tc::poll_bar;
+using tc::warp_poll_bar;
 
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;             // and 10 for half 1
@@ -50,6 +50,7 @@ constexpr int kMinLaunchRegs = 168;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kIssueRegs <= kMinLaunchRegs * kThreads,
               "register split exceeds the launch allocation");
 constexpr uint32_t kTmemCols = 512;
+constexpr int kTurnChunk = 2;               // 32-column chunk after which the turn passes
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 
 template <int D>
@@ -57,7 +58,7 @@ constexpr int ring_slots() { return D == 128 ? 4 : 8; }
 
 struct Maps {
     RowMaps k, v;
-    TileMap q;
+    TileMap q, o;   // o: boxes of 32 rows
 };
 
 struct Shared {
@@ -65,6 +66,7 @@ struct Shared {
     uint64_t full[8], empty[8];       // K/V slots
     uint64_t s_full[2], p_full[2];    // S written / P written
     uint64_t o_full[2], o_free[2];    // O final / read out
+    uint64_t turn[2];                 // half h may exponentiate its next paired tile
     uint64_t drain[2];
     uint32_t tmem_base;
     int abort_flag;
@@ -118,7 +120,7 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ Shared sh;
     const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t sQ = base, sRing = base + 2 * kTile;
+    const uint32_t sQ = base, sRing = base + 2 * kTile, sStage = sRing + NS * kTile;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int h = 0; h < 2; ++h) {
@@ -128,6 +130,7 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
             tc::mbar_init(tc::smem_u32(&sh.p_full[h]), 4);
             tc::mbar_init(tc::smem_u32(&sh.o_full[h]), 1);
             tc::mbar_init(tc::smem_u32(&sh.o_free[h]), 4);
+            tc::mbar_init(tc::smem_u32(&sh.turn[h]), 4);
             tc::mbar_init(tc::smem_u32(&sh.drain[h]), 1);
         }
         for (int s = 0; s < NS; ++s) {
@@ -161,7 +164,7 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
                 for (int h = 0; ok && h < 2; ++h) {
                     if (half_tiles(a, plan, w, h) == 0) continue;
                     if (used[h] > 0 &&
-                        !wait_bar(&sh.q_empty[h], (used[h] - 1) & 1, abort_flag, err, (1 << 16) + h)) {
+                        !poll_bar(&sh.q_empty[h], (used[h] - 1) & 1, abort_flag, err, (1 << 16) + h)) {
                         ok = false;
                         break;
                     }
@@ -169,9 +172,16 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
                                  tc::smem_u32(&sh.q_full[h]));
                     ++used[h];
                 }
+                // the next item's query rows on their way from HBM to L2 meanwhile
+                if (ok && item + (int)gridDim.x < plan.items) {
+                    const Work x = work_item(a, plan, item + gridDim.x);
+                    for (int h = 0; h < 2; ++h)
+                        if (half_tiles(a, plan, x, h) > 0 && !(plan.solo && h))
+                            prefetch_tile<D>(maps.q, x.b, x.h, x.q0 + h * BM);
+                }
                 for (int j = 0; ok && j < 2 * w.T; ++j) {
                     if (fills >= NS &&
-                        !wait_bar(&sh.empty[ring.slot], ring.phase ^ 1, abort_flag, err, (2 << 16) + j)) {
+                        !poll_bar(&sh.empty[ring.slot], ring.phase ^ 1, abort_flag, err, (2 << 16) + j)) {
                         ok = false;
                         break;
                     }
@@ -196,44 +206,75 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
             uint32_t n = 0, tiles = 0;   // items and tiles of this half so far
             bool ok = true;
             auto skip_slot = [&]() {
-                ok = wait_bar(&sh.full[ring.slot], ring.phase, abort_flag, err, (3 << 16) + h);
+                ok = poll_bar(&sh.full[ring.slot], ring.phase, abort_flag, err, (3 << 16) + h);
                 if (ok) tc::mbar_arrive(tc::smem_u32(&sh.empty[ring.slot]));
                 ring.next(NS);
             };
             for (int item = blockIdx.x; ok && item < plan.items; item += gridDim.x) {
                 const Work w = work_item(a, plan, item);
                 const int mine = half_tiles(a, plan, w, h);
-                if (mine > 0) ok = wait_bar(&sh.q_full[h], n & 1, abort_flag, err, (4 << 16) + h);
-                int done = 0;
-                for (int j = 0; ok && j < w.T; ++j) {
-                    if (mine == 0 || (plan.solo && (j & 1) != h)) {
+                int j = 0;   // tile of the ring position
+                // passes the tiles of the other half
+                auto skip_to = [&](int t) {
+                    for (; ok && j < t; ++j) {
                         skip_slot();
                         if (ok) skip_slot();
-                        continue;
                     }
-                    if (!(ok = wait_bar(&sh.full[ring.slot], ring.phase, abort_flag, err, (5 << 16) + j))) break;
-                    tc::fence_after_sync();
-                    mma_dot<D>(tS, sQ + h * kTile, sRing + ring.slot * kTile);
-                    tc::commit(tc::smem_u32(&sh.s_full[h]));
-                    tc::commit(tc::smem_u32(&sh.empty[ring.slot]));
+                };
+                if (mine == 0) {
+                    skip_to(w.T);
+                    continue;
+                }
+                const int step = plan.solo ? 2 : 1;
+                const bool solo = plan.solo != 0;
+                skip_to(solo ? h : 0);
+                ok = ok && poll_bar(&sh.q_full[h], n & 1, abort_flag, err, (4 << 16) + h) &&
+                     poll_bar(&sh.full[ring.slot], ring.phase, abort_flag, err, (5 << 16));
+                if (!ok) break;
+                tc::fence_after_sync();
+                mma_dot<D>(tS, sQ + h * kTile, sRing + ring.slot * kTile);
+                tc::commit(tc::smem_u32(&sh.s_full[h]));
+                tc::commit(tc::smem_u32(&sh.empty[ring.slot]));
+                if (mine == 1) tc::commit(tc::smem_u32(&sh.q_empty[h]));
+                ring.next(NS);
+                for (int i = 0; i < mine; ++i) {
+                    // everything the next two products need but P is waited
+                    // for ahead of it, so that PV and the next QK follow P
+                    // without a pause.  (The ring holds what this waits for:
+                    // V, the other half's K and V when solo, the next K.)
+                    const int vslot = ring.slot;
+                    if (!(ok = poll_bar(&sh.full[vslot], ring.phase, abort_flag, err, (8 << 16) + i))) break;
                     ring.next(NS);
-                    if (++done == mine) tc::commit(tc::smem_u32(&sh.q_empty[h]));
-                    if (!(ok = wait_bar(&sh.p_full[h], tiles & 1, abort_flag, err, (6 << 16) + j))) break;
-                    ++tiles;
+                    ++j;
+                    const bool more = i + 1 < mine;
+                    if (more) {
+                        skip_to(j + step - 1);
+                        if (!ok || !(ok = poll_bar(&sh.full[ring.slot], ring.phase, abort_flag, err, (5 << 16) + i)))
+                            break;
+                    }
                     // the first PV overwrites O: the last item's must be read out
-                    if (done == 1 && n > 0 &&
-                        !(ok = wait_bar(&sh.o_free[h], (n - 1) & 1, abort_flag, err, (7 << 16) + h)))
+                    if (i == 0 && n > 0 &&
+                        !(ok = poll_bar(&sh.o_free[h], (n - 1) & 1, abort_flag, err, (7 << 16) + h)))
                         break;
-                    if (!(ok = wait_bar(&sh.full[ring.slot], ring.phase, abort_flag, err, (8 << 16) + j))) break;
+                    if (!(ok = poll_bar(&sh.p_full[h], tiles & 1, abort_flag, err, (6 << 16) + i))) break;
+                    ++tiles;
                     tc::fence_after_sync();
-                    mma_rows<D>(tO, tS, sRing + ring.slot * kTile, done > 1 ? 1u : 0u);
-                    tc::commit(tc::smem_u32(&sh.empty[ring.slot]));
-                    ring.next(NS);
+                    mma_rows<D>(tO, tS, sRing + vslot * kTile, i > 0 ? 1u : 0u);
+                    if (more) {
+                        mma_dot<D>(tS, sQ + h * kTile, sRing + ring.slot * kTile);
+                        tc::commit(tc::smem_u32(&sh.s_full[h]));
+                        tc::commit(tc::smem_u32(&sh.empty[vslot]));
+                        tc::commit(tc::smem_u32(&sh.empty[ring.slot]));
+                        if (i + 2 == mine) tc::commit(tc::smem_u32(&sh.q_empty[h]));
+                        ring.next(NS);
+                    } else {
+                        tc::commit(tc::smem_u32(&sh.o_full[h]));
+                        tc::commit(tc::smem_u32(&sh.empty[vslot]));
+                    }
                 }
-                if (ok && mine > 0) {
-                    tc::commit(tc::smem_u32(&sh.o_full[h]));
-                    ++n;
-                }
+                if (!ok) break;
+                skip_to(w.T);
+                ++n;
             }
             // every MMA of this thread is complete once its drain flips; if
             // that wait expires TMEM stays allocated and the device's lost
@@ -255,30 +296,41 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
         const int h = warp >> 2, r = tid & 127;
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t tS = lane_base + h * BN, tO = lane_base + 2 * BN + h * D;
-        uint32_t n = 0, tiles = 0;
+        uint32_t n = 0, tiles = 0, turns = 0;
         bool ok = true;
         uint32_t v[BN];
         for (int item = blockIdx.x; ok && item < plan.items; item += gridDim.x) {
             const Work w = work_item(a, plan, item);
             const int mine = half_tiles(a, plan, w, h);
+            const int paired = min(mine, half_tiles(a, plan, w, 1 - h));
             const int row = w.q0 + (plan.solo ? 0 : h * BM) + r;
             float m_use = -INFINITY, l = 0.f;
             for (int i = 0; i < mine; ++i) {
-                if (!(ok = warp_wait_bar(&sh.s_full[h], tiles & 1, abort_flag, err, (10 << 16) + i))) break;
+                if (!(ok = warp_poll_bar(&sh.s_full[h], tiles & 1, abort_flag, err, (10 << 16) + i))) break;
                 ++tiles;
                 tc::fence_after_sync();
                 const int j = w.t0 + (plan.solo ? 2 * i + h : i);
                 const int valid = w.keys - j * BN;
+                if (valid < BN) {
+                    // the batch's last tile: -inf past the keys, rewritten in
+                    // TMEM so that the main path carries no selects
+#pragma unroll 1
+                    for (int c4 = valid / 32; c4 < BN / 32; ++c4) {
+                        uint32_t t[32];
+                        tc::tmem_ld32(tS + c4 * 32, t);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (c4 * 32 + e >= valid) t[e] = __float_as_uint(-INFINITY);
+                        tc::tmem_st32(tS + c4 * 32, t);
+                    }
+                    tc::tmem_st_wait();
+                }
                 tc::tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
                 tc::tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
                 tc::tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&v[64]));
                 tc::tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&v[96]));
                 tc::tmem_ld_wait();
-                if (valid < BN) {
-#pragma unroll
-                    for (int e = 0; e < BN; ++e)
-                        if (e >= valid) v[e] = __float_as_uint(-INFINITY);
-                }
                 float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
                 for (int e = 0; e < BN; e += 8) {
@@ -305,6 +357,13 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
                     m_use = m_new;
                 }
                 const float neg_m = m_use == -INFINITY ? 0.f : -m_use;   // every score -inf so far
+                // the halves take turns on the exp unit
+                if (i < paired) {
+                    if ((h == 1 || turns > 0) &&
+                        !(ok = warp_poll_bar(&sh.turn[h], (turns - 1 + h) & 1, abort_flag, err, (12 << 16) + i)))
+                        break;
+                    ++turns;
+                }
                 uint64_t s01 = 0ull;
                 const uint64_t xs2 = pack2(scale_log2, scale_log2), nm2 = pack2(neg_m, neg_m);
 #pragma unroll
@@ -320,6 +379,8 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
                         pk[e >> 1] = bf16_pair(p0, p1);
                     }
                     tc::tmem_st16(tS + q * 16, pk);
+                    if (q == kTurnChunk && i < paired && lane == 0)
+                        tc::mbar_arrive(tc::smem_u32(&sh.turn[1 - h]));
                 }
                 l += __uint_as_float((uint32_t)s01) + __uint_as_float((uint32_t)(s01 >> 32));
                 if (any) {
@@ -340,7 +401,7 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
             }
             if (!ok) break;
             if (mine > 0) {
-                if (!(ok = warp_wait_bar(&sh.o_full[h], n & 1, abort_flag, err, (11 << 16)))) break;
+                if (!(ok = warp_poll_bar(&sh.o_full[h], n & 1, abort_flag, err, (11 << 16)))) break;
                 tc::fence_after_sync();
                 ++n;
             }
@@ -351,46 +412,43 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
             const size_t rr = ((size_t)w.b * a.Hq + w.h) * a.Nq + row;
             const bool parts = plan.splits > 1 || plan.solo;
             const size_t part = (size_t)(plan.solo ? 2 * w.split + h : w.split) * a.B * a.Hq * a.Nq + rr;
-            bf16* orow = row_ptr<bf16>(a.O, w.b, w.h, row);
             if (write) {
                 if (parts) lse_part[part] = lse;
                 else a.lse[rr] = lse;
             }
-            if (mine > 0 || !parts) {
+            auto free_o = [&]() {
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.o_free[h]));
+            };
+            if (mine == 0) {
+                if (write && !parts) {
+                    uint4* o4 = reinterpret_cast<uint4*>(row_ptr<bf16>(a.O, w.b, w.h, row));
+#pragma unroll 1
+                    for (int c = 0; c < D / 8; ++c) o4[c] = make_uint4(0, 0, 0, 0);
+                }
+            } else if (parts) {
                 uint32_t o[32];
 #pragma unroll 1
                 for (int c4 = 0; c4 < D / 32; ++c4) {
-                    if (mine > 0) {
-                        tc::tmem_ld32(tO + c4 * 32, o);
-                        tc::tmem_ld_wait();
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0;
-                    }
-                    if (write && parts) {
+                    tc::tmem_ld32(tO + c4 * 32, o);
+                    tc::tmem_ld_wait();
+                    if (write) {
                         float4* o4 = reinterpret_cast<float4*>(o_part + part * D + c4 * 32);
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
                             o4[q] = make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
                                                 __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
-                    } else if (write) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            pk[e >> 1] = bf16_pair(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                        uint4* o4 = reinterpret_cast<uint4*>(orow + c4 * 32);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            o4[q] = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
                     }
                 }
-                if (mine > 0) {
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.o_free[h]));
-                }
+                free_o();
+            } else {
+                const int n0 = row - lane;
+                store_rows<D>(maps.o, sStage + warp * 4096, tO, inv, w.b, w.h, n0, n0 < a.Nq, lane, free_o);
             }
         }
+        if (lane == 0) tc::bulk_wait_read<0>();   // shared memory outlives its stores
+        __syncwarp();
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -422,10 +480,11 @@ int launch(const CrossArgs& a, const Plan& plan, float* o_part, float* lse_part,
     }
     if (launch_regs < kMinLaunchRegs) return SVGEAR_ERR_UNSUPPORTED;
     Maps maps;
-    if (!make_tile_map(&maps.q, a.Q, a.B, a.Hq, a.Nq, D) || !make_row_maps(&maps.k, a.K, a.B, a.Hkv, a.Nk, D) ||
+    if (!make_tile_map(&maps.q, a.Q, a.B, a.Hq, a.Nq, D) || !make_tile_map(&maps.o, a.O, a.B, a.Hq, a.Nq, D, 32) ||
+        !make_row_maps(&maps.k, a.K, a.B, a.Hkv, a.Nk, D) ||
         !make_row_maps(&maps.v, a.V, a.B, a.Hkv, a.Nk, D))
         return SVGEAR_ERR_CUDA;
-    const size_t smem = (size_t)(2 + ring_slots<D>()) * (D / 64) * 16384 + 1024;
+    const size_t smem = (size_t)(2 + ring_slots<D>()) * (D / 64) * 16384 + 8 * 4096 + 1024;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return SVGEAR_ERR_CUDA;
     cross_fwd_sm100_kernel<D><<<plan.items < kSms ? plan.items : kSms, kThreads, smem, st>>>(

@@ -33,10 +33,11 @@ inline bool make_row_maps(RowMaps* m, const svgear_tokens& t, int B, int H, int 
         if (!make_tokens_map(&m->box[i], t, B, H, N, D, 1u << i)) return false;
     return true;
 }
-inline bool make_tile_map(TileMap* m, const svgear_tokens& t, int B, int H, int N, int D) {
+inline bool make_tile_map(TileMap* m, const svgear_tokens& t, int B, int H, int N, int D,
+                          int rows = BM) {
     m->hmul = t.stride_h != 0;
     m->bmul = t.stride_b != 0;
-    return make_tokens_map(&m->box, t, B, H, N, D, BM);
+    return make_tokens_map(&m->box, t, B, H, N, D, rows);
 }
 
 // Copies a 128-row tile from row n0 of head (b, h) into shared memory (D / 64
@@ -48,6 +49,14 @@ __device__ __forceinline__ void load_tile(const TileMap& m, uint32_t dst, int b,
 #pragma unroll
     for (int g = 0; g < D / 64; ++g)
         tc::tma_load_4d(dst + g * 16384, &m.box, g * 64, n0, h * m.hmul, b * m.bmul, bar);
+}
+
+// Brings such a tile into L2.
+template <int D>
+__device__ __forceinline__ void prefetch_tile(const TileMap& m, int b, int h, int n0) {
+#pragma unroll
+    for (int g = 0; g < D / 64; ++g)
+        tc::tma_prefetch_4d(&m.box, g * 64, n0, h * m.hmul, b * m.bmul);
 }
 
 // As load_tile, with rows past `keys` (the batch's key count) reading as
@@ -81,6 +90,52 @@ __device__ __forceinline__ void load_key_tile(const RowMaps& m, uint32_t dst, in
         tc::tma_load_4d(t + n * 128, &m.box[k1], g * 64, N, hc, bc, bar);
         if (BN - n != (1 << k1))
             tc::tma_load_4d(t + (BN - (1 << k1)) * 128, &m.box[k1], g * 64, N, hc, bc, bar);
+    }
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Writes 64 bf16 columns (32 packed words) of this thread's row to the warp's
+// 4 KB staging area (32 rows x 128 bytes, 128-byte swizzle).
+__device__ __forceinline__ void stage_row(uint32_t area, int lane, const uint32_t (&pk)[32]) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(area + lane * 128 + ((c ^ (lane & 7)) << 4)),
+                     "r"(pk[4 * c]), "r"(pk[4 * c + 1]), "r"(pk[4 * c + 2]), "r"(pk[4 * c + 3])
+                     : "memory");
+}
+// Writes this thread's row of D fp32 values in tensor memory, times f and
+// rounded to bf16, to row n0 + lane of head (b, h): the warp's 32 rows go
+// through its staging area and a TMA store, so that whole lines reach L2
+// (each lane storing its own row would touch 32 lines per instruction).
+// `map` has boxes of 32 rows; rows past the tensor are left out.  read_done
+// runs once the TMEM columns are in registers.
+template <int D, typename F>
+__device__ __forceinline__ void store_rows(const TileMap& map, uint32_t area, uint32_t taddr, float f, int b,
+                                           int h, int n0, bool any_row, int lane, F read_done) {
+    uint32_t o[D];
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) tc::tmem_ld32(taddr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[c * 32]));
+    tc::tmem_ld_wait();
+    read_done();
+#pragma unroll
+    for (int g = 0; g < D / 64; ++g) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            pk[e] = bf16_pair(__uint_as_float(o[g * 64 + 2 * e]) * f, __uint_as_float(o[g * 64 + 2 * e + 1]) * f);
+        if (lane == 0) tc::bulk_wait_read<0>();   // the area's last store has been read
+        __syncwarp();
+        stage_row(area, lane, pk);
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0 && any_row) {
+            tc::tma_store_4d(&map.box, area, g * 64, n0, h * map.hmul, b * map.bmul);
+            tc::bulk_commit();
+        }
     }
 }
 
@@ -125,10 +180,6 @@ __device__ __forceinline__ void fma2(uint32_t x0, uint32_t x1, uint64_t m, uint6
 __device__ __forceinline__ void add2(uint64_t& s, float p0, float p1) {
     asm("{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\tadd.rn.f32x2 %0, %0, x;\n\t}"
         : "+l"(s) : "f"(p0), "f"(p1));
-}
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // A slot ring's position: slot index and the parity of its current use.

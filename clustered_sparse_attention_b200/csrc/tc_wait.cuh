@@ -49,6 +49,43 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
     }
 }
 
+// As wait_bar, for loops whose waits last a few thousand cycles and whose
+// latency counts: the abort flags and the clock are read every 1024 polls
+// (some 30,000 cycles).  Reading the status word and %globaltimer takes about
+// a thousand cycles, during which a completed barrier goes unseen; at one
+// look per 64 polls that was often on the critical path (cross attention
+// forward: 4,536 -> 3,400 cycles per pair of 128 x 128 tiles).
+__device__ __forceinline__ bool poll_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                         int* err, int where) {
+    const uint32_t b = smem_u32(bar);
+    uint64_t t0 = 0;
+    volatile int* gerr = err;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(b, parity)) return true;
+        if ((it & 1023) != 0) continue;
+        if (*abort_flag || *gerr) {
+            *abort_flag = 1;
+            return false;
+        }
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitTimeoutNs || it >= kMaxSpins) {
+            *abort_flag = 1;
+            if (atomicCAS(err, 0, SVGEAR_ERR_TIMEOUT) == 0) {
+                err[1] = where;
+                err[2] = (int)(blockIdx.y * 65536 + blockIdx.x);
+            }
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool warp_poll_bar(uint64_t* bar, uint32_t parity,
+                                              volatile int* abort_flag, int* err, int where) {
+    int ok = 0;
+    if ((threadIdx.x & 31) == 0) ok = poll_bar(bar, parity, abort_flag, err, where) ? 1 : 0;
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
 // As wait_bar for copies or MMAs already issued, while a kernel gives up: it
 // ignores the abort flags and only the clock ends it.
 __device__ __forceinline__ bool drain_bar(uint64_t* bar, uint32_t parity) {
