@@ -73,12 +73,6 @@ struct Shared {
     int keep_tmem;
 };
 
-struct Work {
-    int b, h, hk, q0, keys;
-    int t0, T;        // first key tile and number of tiles of the item
-    int split;
-};
-
 struct Plan {
     int qpairs;       // 256-row pairs per head
     int splits;       // key splits
@@ -87,21 +81,45 @@ struct Plan {
     int items;
 };
 
-__device__ __forceinline__ Work work_item(const CrossArgs& a, const Plan& p, int item) {
-    Work w;
-    const int qp = item % p.qpairs;
-    const int r = item / p.qpairs;
-    w.split = r % p.splits;
-    const int bh = r / p.splits;
-    w.b = bh / a.Hq;
-    w.h = bh - w.b * a.Hq;
-    w.hk = w.h / a.G;
-    w.q0 = qp * 2 * BM;
-    w.keys = cross_keys(a, w.b);
-    w.t0 = w.split * p.tiles;
-    w.T = max(0, min((w.keys + BN - 1) / BN - w.t0, p.tiles));
-    return w;
-}
+// The items of one CTA in turn: item = ((b * Hq + h) * splits + split) * qpairs +
+// pair, advanced by the grid digit by digit (divisions once per CTA: they
+// would sit on every role's path between items).
+struct Work {
+    int item, qp, split, h, b;        // digits
+    int dq, ds, dh, db;               // the grid's digits
+    int hk, q0, keys;
+    int t0, T;                        // first key tile and number of tiles
+    __device__ __forceinline__ void derive(const CrossArgs& a, const Plan& p) {
+        q0 = qp * 2 * BM;
+        keys = cross_keys(a, b);
+        t0 = split * p.tiles;
+        T = max(0, min((keys + BN - 1) / BN - t0, p.tiles));
+        hk = a.G == 1 ? h : h / a.G;
+    }
+    __device__ __forceinline__ void start(const CrossArgs& a, const Plan& p) {
+        item = blockIdx.x;
+        int x = item;
+        qp = x % p.qpairs; x /= p.qpairs;
+        split = x % p.splits; x /= p.splits;
+        h = x % a.Hq;
+        b = x / a.Hq;
+        x = gridDim.x;
+        dq = x % p.qpairs; x /= p.qpairs;
+        ds = x % p.splits; x /= p.splits;
+        dh = x % a.Hq;
+        db = x / a.Hq;
+        if (item < p.items) derive(a, p);
+    }
+    __device__ __forceinline__ void next(const CrossArgs& a, const Plan& p) {
+        item += gridDim.x;
+        qp += dq; split += ds; h += dh; b += db;
+        if (qp >= p.qpairs) { qp -= p.qpairs; ++split; }
+        if (split >= p.splits) { split -= p.splits; ++h; }
+        if (h >= a.Hq) { h -= a.Hq; ++b; }
+        if (item < p.items) derive(a, p);
+    }
+};
+
 // Tiles that half h takes of an item (0: the half sits it out).
 __device__ __forceinline__ int half_tiles(const CrossArgs& a, const Plan& p, const Work& w, int h) {
     if (p.solo) return (w.T + 1 - h) / 2;
@@ -159,8 +177,8 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
             uint32_t fills = 0;          // slots filled so far
             uint32_t used[2] = {0, 0};   // Q tiles loaded per half
             bool ok = true;
-            for (int item = blockIdx.x; ok && item < plan.items; item += gridDim.x) {
-                const Work w = work_item(a, plan, item);
+            Work w;
+            for (w.start(a, plan); ok && w.item < plan.items; w.next(a, plan)) {
                 for (int h = 0; ok && h < 2; ++h) {
                     if (half_tiles(a, plan, w, h) == 0) continue;
                     if (used[h] > 0 &&
@@ -173,8 +191,9 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
                     ++used[h];
                 }
                 // the next item's query rows on their way from HBM to L2 meanwhile
-                if (ok && item + (int)gridDim.x < plan.items) {
-                    const Work x = work_item(a, plan, item + gridDim.x);
+                if (ok && w.item + (int)gridDim.x < plan.items) {
+                    Work x = w;
+                    x.next(a, plan);
                     for (int h = 0; h < 2; ++h)
                         if (half_tiles(a, plan, x, h) > 0 && !(plan.solo && h))
                             prefetch_tile<D>(maps.q, x.b, x.h, x.q0 + h * BM);
@@ -210,8 +229,8 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
                 if (ok) tc::mbar_arrive(tc::smem_u32(&sh.empty[ring.slot]));
                 ring.next(NS);
             };
-            for (int item = blockIdx.x; ok && item < plan.items; item += gridDim.x) {
-                const Work w = work_item(a, plan, item);
+            Work w;
+            for (w.start(a, plan); ok && w.item < plan.items; w.next(a, plan)) {
                 const int mine = half_tiles(a, plan, w, h);
                 int j = 0;   // tile of the ring position
                 // passes the tiles of the other half
@@ -299,8 +318,8 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
         uint32_t n = 0, tiles = 0, turns = 0;
         bool ok = true;
         uint32_t v[BN];
-        for (int item = blockIdx.x; ok && item < plan.items; item += gridDim.x) {
-            const Work w = work_item(a, plan, item);
+        Work w;
+        for (w.start(a, plan); ok && w.item < plan.items; w.next(a, plan)) {
             const int mine = half_tiles(a, plan, w, h);
             const int paired = min(mine, half_tiles(a, plan, w, 1 - h));
             const int row = w.q0 + (plan.solo ? 0 : h * BM) + r;

@@ -50,33 +50,39 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
 }
 
 // As wait_bar, for loops whose waits last a few thousand cycles and whose
-// latency counts: the abort flags and the clock are read every 1024 polls
-// (some 30,000 cycles).  Reading the status word and %globaltimer takes about
-// a thousand cycles, during which a completed barrier goes unseen; at one
-// look per 64 polls that was often on the critical path (cross attention
-// forward: 4,536 -> 3,400 cycles per pair of 128 x 128 tiles).
+// latency counts: the abort flags and the clock are read every 1024 polls (some
+// 30,000 cycles).  Reading the status word and %globaltimer takes long enough
+// that a barrier completed meanwhile goes unseen on the critical path (cross
+// attention forward, 75,600 x 512 keys: 930 us with a look every 64 polls, 873
+// with this).
+// The slow look, one copy for all waits of a kernel (inlined, it made up a third
+// of its code).  Returns true to go on polling; *t0 is the first look's time.
+static __device__ __noinline__ bool poll_look(uint64_t* t0, volatile int* abort_flag, int* err, int where,
+                                              uint32_t it) {
+    if (*abort_flag || *(volatile int*)err) {
+        *abort_flag = 1;
+        return false;
+    }
+    const uint64_t now = global_timer_ns();
+    if (*t0 == 0) *t0 = now;
+    if (now - *t0 > kWaitTimeoutNs || it >= kMaxSpins) {
+        *abort_flag = 1;
+        if (atomicCAS(err, 0, SVGEAR_ERR_TIMEOUT) == 0) {
+            err[1] = where;
+            err[2] = (int)(blockIdx.y * 65536 + blockIdx.x);
+        }
+        return false;
+    }
+    return true;
+}
 __device__ __forceinline__ bool poll_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                          int* err, int where) {
     const uint32_t b = smem_u32(bar);
     uint64_t t0 = 0;
-    volatile int* gerr = err;
+#pragma unroll 1
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(b, parity)) return true;
-        if ((it & 1023) != 0) continue;
-        if (*abort_flag || *gerr) {
-            *abort_flag = 1;
-            return false;
-        }
-        const uint64_t now = global_timer_ns();
-        if (t0 == 0) t0 = now;
-        if (now - t0 > kWaitTimeoutNs || it >= kMaxSpins) {
-            *abort_flag = 1;
-            if (atomicCAS(err, 0, SVGEAR_ERR_TIMEOUT) == 0) {
-                err[1] = where;
-                err[2] = (int)(blockIdx.y * 65536 + blockIdx.x);
-            }
-            return false;
-        }
+        if (mbar_test(b, parity)) return true;
+        if ((it & 1023) == 0 && !poll_look(&t0, abort_flag, err, where, it)) return false;
     }
 }
 __device__ __forceinline__ bool warp_poll_bar(uint64_t* bar, uint32_t parity,
