@@ -93,6 +93,8 @@ __device__ __forceinline__ int64_t kv_range(int64_t total, int c, int ctas) {
 
 // Rows per CTA and keys per tile of the SIMT kernels.
 constexpr int kCrossSimtM = 64, kCrossSimtN = 64;
+// Keys per tile of the tensor-core kernels.
+constexpr int kCrossTcN = 128;
 
 // How a forward call is cut: few (head, row tile) items over many keys are
 // split along the keys, each split leaving a partial O and lse for the join.
@@ -124,8 +126,12 @@ struct HeldTokens {
 };
 int launch_cross_delta(const CrossArgs& a, int dtype, const HeldTokens* q, const HeldTokens* o,
                        void* qx, cudaStream_t st);
-int launch_cross_dq_simt(const CrossArgs& a, int dtype, cudaStream_t st);
-int launch_cross_dkv_simt(const CrossArgs& a, int dtype, int ctas, float* part, cudaStream_t st);
+int launch_cross_backward_simt(const CrossArgs& a, int ctas, float* part, cudaStream_t st);   // fp32
+int launch_cross_backward_sm100(const CrossArgs& a, float* part, int* err, cudaStream_t st);  // bf16
+// Joins the parts of the dK/dV pass (see above); keys: rows of a key tile
+// (kCrossSimtN for fp32, kCrossTcN for bf16), rows: of a query tile.
+int launch_cross_dkv_join(const CrossArgs& a, int dtype, int rows, int ctas, const float* part,
+                          cudaStream_t st);
 
 int launch_checkpoint_save(svgear_tokens X, svgear_dims dims, int8_t* codes, uint8_t* exps,
                            cudaStream_t st);

@@ -124,7 +124,7 @@ BwdWs carve_bwd(Carve& cv, const svgear_cross_dims& d, bool held) {
     w.status = cv.take<int>(4);
     w.delta = cv.take<float>(rows_of(d));
     w.qx = cv.take<char>(held ? rows_of(d) * d.d * (d.dtype == SVGEAR_F32 ? 4 : 2) : 0);
-    w.part = cv.take<float>((size_t)kSms * 2 * 2 * kCrossSimtN * d.d);
+    w.part = cv.take<float>((size_t)kSms * 2 * 2 * (d.dtype == SVGEAR_BF16 ? kCrossTcN : kCrossSimtN) * d.d);
     return w;
 }
 
@@ -165,8 +165,8 @@ int backward(svgear_tokens dO, svgear_tokens Q, const HeldTokens* qh, svgear_tok
     a.delta = w.delta;
     if (cudaMemsetAsync(w.status, 0, 4 * sizeof(int), st) != cudaSuccess) return SVGEAR_ERR_CUDA;
     if ((s = launch_cross_delta(a, dims.dtype, qh, oh, w.qx, st))) return s;
-    if ((s = launch_cross_dq_simt(a, dims.dtype, st))) return s;
-    return launch_cross_dkv_simt(a, dims.dtype, kSms, w.part, st);
+    return dims.dtype == SVGEAR_BF16 ? launch_cross_backward_sm100(a, w.part, w.status, st)
+                                     : launch_cross_backward_simt(a, kSms, w.part, st);
 }
 
 int check_token_dims(const svgear_dims& d) {

@@ -1,0 +1,788 @@
+// cross_bwd_sm100.cu -- gradients of the dense cross attention for bf16 tokens
+// on tcgen05 / TMEM (sm_100a), from the forward pass's lse and delta = do.o:
+//   p_ij = e^{s_ij - lse_i}, ds_ij = p_ij (do_i.v_j - delta_i),
+//   dq_i = scale sum_j ds_ij k_j, dk_j = scale sum_i ds_ij q_i,
+//   dv_j = sum_i p_ij do_i.
+// p and ds enter their second product rounded to bf16 (an error of the size of
+// the outputs' own rounding); everything else, all sums among it, is fp32.
+//
+// Two kernels, each recomputing the scores from Q and K: one keeps a key tile
+// and walks the queries (dK, dV), the other keeps a query tile and walks the
+// keys (dQ).  One kernel for all three would need five products per tile pair
+// instead of seven, but dQ sums over key tiles that other CTAs hold: by atomics
+// its result would change from run to run, and TMEM has no room for it (S, dP,
+// dV and dK fill the 512 columns).
+//
+// Roles and barriers are those of the forward kernel: two warpgroups turn score
+// tiles into weights, each 64 of a tile's 128 columns, one row per thread; one
+// thread per chain of products issues its MMAs; one thread copies tiles by TMA.
+// Every wait is bounded (tc_wait.cuh).
+#include <math.h>
+
+#include "cross_tc.cuh"
+#include "launchers.h"
+
+namespace svgear {
+namespace crosstc {
+namespace {
+
+using bf16 = __nv_bfloat16;
+using tc::poll_bar;
+using tc::warp_poll_bar;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int HN = 64;   // columns of a tile per warpgroup
+constexpr uint32_t kTmemCols = 512;
+
+// Rewrites columns >= valid of this warp's HN score columns at taddr to -inf.
+__device__ __forceinline__ void mask_columns(uint32_t taddr, int valid) {
+#pragma unroll 1
+    for (int c4 = max(valid, 0) / 32; c4 < HN / 32; ++c4) {
+        uint32_t t[32];
+        tc::tmem_ld32(taddr + c4 * 32, t);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (c4 * 32 + e >= valid) t[e] = __float_as_uint(-INFINITY);
+        tc::tmem_st32(taddr + c4 * 32, t);
+    }
+    tc::tmem_st_wait();
+}
+// (a, b) - (c, c) on packed fp32 pairs
+__device__ __forceinline__ uint64_t sub2(uint32_t a, uint32_t b, uint64_t neg) {
+    uint64_t r;
+    asm("{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\tadd.rn.f32x2 %0, x, %3;\n\t}"
+        : "=l"(r) : "r"(a), "r"(b), "l"(neg));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float lo(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float hi(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+
+// One thread's MMAs are complete once `bar` flips; if that wait expires TMEM
+// stays allocated and the device's lost word stops every later tensor-core
+// kernel before it allocates.
+__device__ __forceinline__ void drain_mma(uint64_t* bar, int* keep_tmem, int* err, int* lost, int where) {
+    tc::commit(tc::smem_u32(bar));
+    if (!tc::drain_bar(bar, 0)) {
+        *keep_tmem = 1;
+        tc::mark_tmem_lost(lost);
+        if (atomicCAS(err, 0, SVGEAR_ERR_TIMEOUT) == 0) {
+            err[1] = where;
+            err[2] = blockIdx.x;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dK, dV: a persistent CTA per SM takes an equal share of the iterations (key
+// tile, query head, query tile); see KvUnit.  K and V of the unit stay in
+// shared memory; Q and dO tiles stream through a ring, with lse and delta of
+// their rows.  Rows (TMEM lanes) are keys, columns queries:
+//   chain A: S^T = K Q^T -> P^T (over S^T) -> dV += P^T dO
+//   chain B: dP^T = V dO^T -> dS^T (over dP^T) -> dK += dS^T Q
+// each issued by its own thread, so that S(i + 1) follows dV(i), dP(i + 1)
+// follows dK(i), and either runs beside the other chain's arithmetic.
+// TMEM: S | dP | dV | dK.
+// ---------------------------------------------------------------------------
+constexpr int kKvThreads = 12 * 32;   // 0-7 weights, 8 TMA, 9 and 10 MMA chains, 11 lse and delta
+
+template <int D>
+constexpr int kv_stages() { return D == 128 ? 2 : 4; }
+template <int D>
+constexpr uint32_t kv_smem() { return (2 + 2 * kv_stages<D>()) * (D / 64) * 16384 + 1024; }
+
+struct KvMaps {
+    TileMap q, g, k, v;
+};
+
+struct KvShared {
+    uint64_t kv_full;
+    uint64_t full[4], empty[4];
+    uint64_t s_full, p_full, dp_full, ds_full;
+    uint64_t acc_full, acc_free;
+    uint64_t drain[2];
+    alignas(16) float neg_lse2[4][BM];   // -lse log2 e of the stage's rows
+    alignas(16) float neg_delta[4][BM];
+    uint32_t tmem_base;
+    int abort_flag;
+    int keep_tmem;
+};
+
+// A CTA's share as pieces of units.
+struct Pieces {
+    int64_t it, end, per;
+    KvCursor cur;
+    KvUnit k;
+    int64_t first, last;   // iterations of the unit in this piece
+    __device__ __forceinline__ Pieces(const CrossArgs& a, int64_t units) {
+        per = (int64_t)a.G * ((a.Nq + BM - 1) / BM);
+        const int64_t total = units * per;
+        it = kv_range(total, blockIdx.x, gridDim.x);
+        end = kv_range(total, blockIdx.x + 1, gridDim.x);
+        kv_cursor_start<BN>(a, cur);
+    }
+    __device__ __forceinline__ bool next(const CrossArgs& a) {
+        if (it >= end) return false;
+        const int64_t u = it / per;
+        first = it - u * per;
+        last = min(per, first + (end - it));
+        k = kv_unit<BN>(a, cur, u);
+        it += last - first;
+        return true;
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kKvThreads, 1)
+cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* __restrict__ part,
+                       int* __restrict__ err, int* __restrict__ lost) {
+    constexpr uint32_t kTile = (D / 64) * 16384;
+    constexpr int NS = kv_stages<D>();
+    if (tc::refuse_start(lost, err)) return;
+
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ KvShared sh;
+    const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t sK = base, sV = sK + kTile, sRing = sV + kTile;   // stage: Q, dO
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t units = kv_total_units<BN>(a);
+    if (tid == 0) {
+        tc::mbar_init(tc::smem_u32(&sh.kv_full), 2);
+        for (int s = 0; s < NS; ++s) {
+            tc::mbar_init(tc::smem_u32(&sh.full[s]), 3);    // Q, dO, lse and delta
+            tc::mbar_init(tc::smem_u32(&sh.empty[s]), 2);   // both chains
+        }
+        tc::mbar_init(tc::smem_u32(&sh.s_full), 1);
+        tc::mbar_init(tc::smem_u32(&sh.p_full), 8);
+        tc::mbar_init(tc::smem_u32(&sh.dp_full), 1);
+        tc::mbar_init(tc::smem_u32(&sh.ds_full), 8);
+        tc::mbar_init(tc::smem_u32(&sh.acc_full), 2);
+        tc::mbar_init(tc::smem_u32(&sh.acc_free), 8);
+        tc::mbar_init(tc::smem_u32(&sh.drain[0]), 1);
+        tc::mbar_init(tc::smem_u32(&sh.drain[1]), 1);
+        sh.abort_flag = 0;
+        sh.keep_tmem = 0;
+        tc::mbar_init_fence();
+    }
+    if (warp == 9) {
+        tc::tmem_alloc(tc::smem_u32(&sh.tmem_base), kTmemCols);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sh.tmem_base;
+    volatile int* abort_flag = &sh.abort_flag;
+    const int qtiles = (a.Nq + BM - 1) / BM;
+    const float scale_log2 = a.scale * kLog2e;
+    Pieces p(a, units);
+
+    if (warp == 8 && lane == 0) {
+        // ------------------------------------------------------------ producer
+        Ring ring;
+        uint32_t fills = 0, n = 0;
+        bool ok = true;
+        while (ok && p.next(a)) {
+            // the last unit's products have read K and V
+            if (n > 0 && !(ok = poll_bar(&sh.acc_full, (n - 1) & 1, abort_flag, err, (1 << 16)))) break;
+            load_tile<D>(maps.k, sK, p.k.b, p.k.h, p.k.kt * BN, tc::smem_u32(&sh.kv_full));
+            load_tile<D>(maps.v, sV, p.k.b, p.k.h, p.k.kt * BN, tc::smem_u32(&sh.kv_full));
+            ++n;
+            int g = (int)(p.first / qtiles), qt = (int)(p.first - (int64_t)g * qtiles);
+            for (int64_t x = p.first; x < p.last; ++x) {
+                if (fills >= NS && !(ok = poll_bar(&sh.empty[ring.slot], ring.phase ^ 1, abort_flag, err, (2 << 16))))
+                    break;
+                const uint32_t bar = tc::smem_u32(&sh.full[ring.slot]), dst = sRing + ring.slot * 2 * kTile;
+                load_tile<D>(maps.q, dst, p.k.b, p.k.h * a.G + g, qt * BM, bar);
+                load_tile<D>(maps.g, dst + kTile, p.k.b, p.k.h * a.G + g, qt * BM, bar);
+                ++fills;
+                ring.next(NS);
+                if (++qt == qtiles) {
+                    qt = 0;
+                    ++g;
+                }
+            }
+        }
+        // gave up: let the copies in flight land before the CTA ends (a stage
+        // whose lse never came is bounded by the clock)
+        if (!ok) {
+            if (n > 0) tc::drain_bar(&sh.kv_full, (n - 1) & 1);
+            for (uint32_t f = fills > NS ? fills - NS : 0; f < fills; ++f)
+                tc::drain_bar(&sh.full[f % NS], (f / NS) & 1);
+        }
+    } else if (warp == 11) {
+        // -------------------------------------------------------- lse and delta
+        Ring ring;
+        uint32_t fills = 0;
+        bool ok = true;
+        while (ok && p.next(a)) {
+            int g = (int)(p.first / qtiles), qt = (int)(p.first - (int64_t)g * qtiles);
+            for (int64_t x = p.first; x < p.last; ++x) {
+                const size_t r0 = ((size_t)p.k.b * a.Hq + p.k.h * a.G + g) * a.Nq + (size_t)qt * BM;
+                float l[4], d[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {   // rows past the end: p = e^{-inf} = 0
+                    const bool in = qt * BM + 32 * i + lane < a.Nq;
+                    l[i] = in ? __ldg(a.lse + r0 + 32 * i + lane) * -kLog2e : -INFINITY;
+                    d[i] = in ? -__ldg(a.delta + r0 + 32 * i + lane) : 0.f;
+                }
+                if (fills >= NS &&
+                    !(ok = warp_poll_bar(&sh.empty[ring.slot], ring.phase ^ 1, abort_flag, err, (3 << 16))))
+                    break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sh.neg_lse2[ring.slot][32 * i + lane] = l[i];
+                    sh.neg_delta[ring.slot][32 * i + lane] = d[i];
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.full[ring.slot]));
+                ++fills;
+                ring.next(NS);
+                if (++qt == qtiles) {
+                    qt = 0;
+                    ++g;
+                }
+            }
+        }
+    } else if (warp >= 9 && lane == 0) {
+        // --------------------------------------------------- MMA chains A and B
+        const bool chain_a = warp == 9;
+        uint64_t* sc_full = chain_a ? &sh.s_full : &sh.dp_full;    // score tile written
+        uint64_t* w_full = chain_a ? &sh.p_full : &sh.ds_full;     // weights written over it
+        const uint32_t tW = tmem + (chain_a ? 0 : BN), tAcc = tmem + 2 * BN + (chain_a ? 0 : D);
+        const uint32_t sStat = chain_a ? sK : sV;
+        const uint32_t score_off = chain_a ? 0 : kTile;   // Q for S, dO for dP
+        const uint32_t acc_off = chain_a ? kTile : 0;     // dO for dV, Q for dK
+        Ring ring;
+        uint32_t n = 0, i = 0;
+        bool ok = true;
+        while (ok && p.next(a)) {
+            ok = poll_bar(&sh.kv_full, n & 1, abort_flag, err, (4 << 16)) &&
+                 poll_bar(&sh.full[ring.slot], ring.phase, abort_flag, err, (5 << 16));
+            if (!ok) break;
+            tc::fence_after_sync();
+            mma_dot<D>(tW, sStat, sRing + ring.slot * 2 * kTile + score_off);
+            tc::commit(tc::smem_u32(sc_full));
+            // the first sum overwrites the accumulator: the last must be read out
+            if (n > 0 && !(ok = poll_bar(&sh.acc_free, (n - 1) & 1, abort_flag, err, (6 << 16)))) break;
+            for (int64_t x = p.first; x < p.last; ++x, ++i) {
+                const uint32_t cur = sRing + ring.slot * 2 * kTile;
+                uint64_t* cur_empty = &sh.empty[ring.slot];
+                ring.next(NS);
+                const bool more = x + 1 < p.last;
+                if (more && !(ok = poll_bar(&sh.full[ring.slot], ring.phase, abort_flag, err, (5 << 16)))) break;
+                if (!(ok = poll_bar(w_full, i & 1, abort_flag, err, (7 << 16)))) break;
+                tc::fence_after_sync();
+                mma_rows64<D>(tAcc, tW, cur + acc_off, x > p.first ? 1u : 0u);
+                mma_rows64<D>(tAcc, tW + HN, cur + acc_off + HN * 128, 1u);
+                if (more) {
+                    mma_dot<D>(tW, sStat, sRing + ring.slot * 2 * kTile + score_off);
+                    tc::commit(tc::smem_u32(sc_full));
+                }
+                tc::commit(tc::smem_u32(cur_empty));
+            }
+            if (!ok) break;
+            tc::commit(tc::smem_u32(&sh.acc_full));
+            ++n;
+        }
+        drain_mma(&sh.drain[chain_a ? 0 : 1], &sh.keep_tmem, err, lost, (9 << 16) + (chain_a ? 0 : 1));
+    } else if (warp < 8) {
+        // -------------------------------------------------------------- weights
+        const int h = warp >> 2, r = tid & 127;
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t tS = lane_base + h * HN, tP = lane_base + BN + h * HN;
+        const uint64_t xs2 = pack2(scale_log2, scale_log2);
+        Ring ring;
+        uint32_t n = 0, i = 0;
+        bool ok = true;
+        while (ok && p.next(a)) {
+            for (int64_t x = p.first; x < p.last; ++x, ++i) {
+                if (!(ok = warp_poll_bar(&sh.full[ring.slot], ring.phase, abort_flag, err, (10 << 16)) &&
+                           warp_poll_bar(&sh.s_full, i & 1, abort_flag, err, (11 << 16))))
+                    break;
+                tc::fence_after_sync();
+                const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(&sh.neg_lse2[ring.slot][h * HN]);
+                const ulonglong2* nd = reinterpret_cast<const ulonglong2*>(&sh.neg_delta[ring.slot][h * HN]);
+                uint32_t v[HN];
+                tc::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+                tc::tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+                tc::tmem_ld_wait();
+                // P^T = 2^(s scale log2 e - lse log2 e)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const ulonglong2 l4 = nl[q * 8 + e / 4];
+                        uint32_t* y = &v[q * 32 + e];
+                        fma2(y[0], y[1], xs2, l4.x, y[0], y[1]);
+                        fma2(y[2], y[3], xs2, l4.y, y[2], y[3]);
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) y[z] = __float_as_uint(tc::ex2(__uint_as_float(y[z])));
+                        pk[e / 2] = bf16_pair(__uint_as_float(y[0]), __uint_as_float(y[1]));
+                        pk[e / 2 + 1] = bf16_pair(__uint_as_float(y[2]), __uint_as_float(y[3]));
+                    }
+                    tc::tmem_st16(tS + q * 16, pk);
+                }
+                tc::tmem_st_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.p_full));
+                if (!(ok = warp_poll_bar(&sh.dp_full, i & 1, abort_flag, err, (12 << 16)))) break;
+                tc::fence_after_sync();
+                // dS^T = P^T (dP^T - delta)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t d[32], pk[16];
+                    tc::tmem_ld32(tP + q * 32, d);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const ulonglong2 d4 = nd[q * 8 + e / 4];
+                        const uint32_t* y = &v[q * 32 + e];
+                        const uint64_t s0 = mul2(sub2(d[e], d[e + 1], d4.x),
+                                                 (uint64_t)y[0] | ((uint64_t)y[1] << 32));
+                        const uint64_t s1 = mul2(sub2(d[e + 2], d[e + 3], d4.y),
+                                                 (uint64_t)y[2] | ((uint64_t)y[3] << 32));
+                        pk[e / 2] = bf16_pair(lo(s0), hi(s0));
+                        pk[e / 2 + 1] = bf16_pair(lo(s1), hi(s1));
+                    }
+                    tc::tmem_st16(tP + q * 16, pk);
+                }
+                tc::tmem_st_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.ds_full));
+                ring.next(NS);
+            }
+            if (!ok) break;
+            // the unit's sums (or this CTA's part of them): warpgroup 0 writes
+            // dV, warpgroup 1 dK
+            if (!(ok = warp_poll_bar(&sh.acc_full, n & 1, abort_flag, err, (13 << 16)))) break;
+            tc::fence_after_sync();
+            ++n;
+            const bool whole = p.first == 0 && p.last == p.per;
+            const float f = h == 0 ? 1.f : a.scale;
+            const int row = p.k.kt * BN + r;
+            float* dst_part = part + ((((size_t)blockIdx.x * 2 + (p.first == 0 ? 1 : 0)) * 2 + (1 - h)) * BN + r) * D;
+            bf16* dst = row_ptr<bf16>(h == 0 ? a.dV : a.dK, p.k.b, p.k.h, row);
+            const uint32_t tA = lane_base + 2 * BN + h * D;
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tc::tmem_ld16(tA + c * 16, o);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                if (!whole) {
+                    uint4* o4 = reinterpret_cast<uint4*>(dst_part + c * 16);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        o4[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                } else if (row < p.k.keys) {
+                    uint32_t pk[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        pk[e] = bf16_pair(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                    uint4* o4 = reinterpret_cast<uint4*>(dst + c * 16);
+                    o4[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    o4[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                }
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.acc_free));
+        }
+    }
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 9 && !sh.keep_tmem) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+// ---------------------------------------------------------------------------
+// dQ: an item is 128 query rows of one head; a persistent CTA per SM takes
+// items in turn.  Q and dO of the item stay in shared memory, K and V tiles
+// stream through two rings.  Rows (TMEM lanes) are queries, columns keys:
+//   S = Q K^T (two buffers), dP = dO V^T, dS = p (dP - delta) over S, dQ += dS K.
+// One thread issues dP(j + 1) and then dQ(j) when dS(j) is written, another
+// S(j + 2) when dQ(j) has read dS(j) out of its buffer, so the weights of j + 1
+// are computed meanwhile.  TMEM: S[0] | S[1] | dP | dQ.
+// ---------------------------------------------------------------------------
+constexpr int kQThreads = 16 * 32;   // 0-7 weights, 8 TMA, 9 S, 10 dP and dQ, 12-15 epilogue
+
+template <int D>
+constexpr int q_slots() { return D == 128 ? 2 : 4; }
+template <int D>
+constexpr uint32_t q_smem() { return (2 + 2 * q_slots<D>()) * (D / 64) * 16384 + 4 * 8192 + 1024; }
+
+struct QMaps {
+    RowMaps k, v;
+    TileMap q, g, dq;   // dq: boxes of 32 rows
+};
+
+struct QShared {
+    uint64_t q_full, q_empty, g_full, g_empty;
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t s_full[2], s_free[2];
+    uint64_t dp_full, ds_full;
+    uint64_t acc_full, acc_free;
+    uint64_t drain[2];
+    uint32_t tmem_base;
+    int abort_flag;
+    int keep_tmem;
+};
+
+// The items of one CTA: item = (b * Hq + h) * qtiles + tile, advanced by the
+// grid digit by digit.
+struct QItem {
+    int item, qt, h, b, dq, dh, db, qtiles, items;
+    int hk, keys, T;
+    __device__ __forceinline__ void derive(const CrossArgs& a) {
+        keys = cross_keys(a, b);
+        T = (keys + BN - 1) / BN;
+        hk = a.G == 1 ? h : h / a.G;
+    }
+    __device__ __forceinline__ bool start(const CrossArgs& a) {
+        qtiles = (a.Nq + BM - 1) / BM;
+        items = a.B * a.Hq * qtiles;
+        item = blockIdx.x;
+        int x = item;
+        qt = x % qtiles; x /= qtiles;
+        h = x % a.Hq;
+        b = x / a.Hq;
+        x = gridDim.x;
+        dq = x % qtiles; x /= qtiles;
+        dh = x % a.Hq;
+        db = x / a.Hq;
+        if (item < items) derive(a);
+        return item < items;
+    }
+    __device__ __forceinline__ bool next(const CrossArgs& a) {
+        item += gridDim.x;
+        qt += dq; h += dh; b += db;
+        if (qt >= qtiles) { qt -= qtiles; ++h; }
+        if (h >= a.Hq) { h -= a.Hq; ++b; }
+        if (item < items) derive(a);
+        return item < items;
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kQThreads, 1)
+cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __restrict__ err,
+                      int* __restrict__ lost) {
+    constexpr uint32_t kTile = (D / 64) * 16384;
+    constexpr int NS = q_slots<D>();
+    if (tc::refuse_start(lost, err)) return;
+
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ QShared sh;
+    const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t sQ = base, sG = sQ + kTile, sK = sG + kTile, sV = sK + NS * kTile, sStage = sV + NS * kTile;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        uint64_t* one[] = {&sh.q_full, &sh.q_empty, &sh.g_full, &sh.g_empty, &sh.dp_full,
+                           &sh.acc_full, &sh.drain[0], &sh.drain[1]};
+        for (uint64_t* x : one) tc::mbar_init(tc::smem_u32(x), 1);
+        tc::mbar_init(tc::smem_u32(&sh.ds_full), 8);
+        tc::mbar_init(tc::smem_u32(&sh.acc_free), 4);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(tc::smem_u32(&sh.s_full[i]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.s_free[i]), 1);
+        }
+        for (int i = 0; i < NS; ++i) {
+            tc::mbar_init(tc::smem_u32(&sh.k_full[i]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.k_empty[i]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.v_full[i]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.v_empty[i]), 1);
+        }
+        sh.abort_flag = 0;
+        sh.keep_tmem = 0;
+        tc::mbar_init_fence();
+    }
+    if (warp == 9) {
+        tc::tmem_alloc(tc::smem_u32(&sh.tmem_base), kTmemCols);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sh.tmem_base;
+    volatile int* abort_flag = &sh.abort_flag;
+    QItem w;
+
+    if (warp == 8 && lane == 0) {
+        // ------------------------------------------------------------ producer
+        Ring ring;
+        uint32_t kfills = 0, vfills = 0, n = 0;
+        bool ok = true, q_loaded = false, g_loaded = false;
+        for (bool more = w.start(a); ok && more; more = w.next(a)) {
+            if (w.T == 0) continue;
+            q_loaded = g_loaded = false;
+            if (n > 0 && !(ok = poll_bar(&sh.q_empty, (n - 1) & 1, abort_flag, err, (1 << 16)))) break;
+            load_tile<D>(maps.q, sQ, w.b, w.h, w.qt * BM, tc::smem_u32(&sh.q_full));
+            q_loaded = true;
+            for (int j = 0; j < w.T; ++j) {
+                if (kfills >= NS && !(ok = poll_bar(&sh.k_empty[ring.slot], ring.phase ^ 1, abort_flag, err, (2 << 16))))
+                    break;
+                load_key_tile<D>(maps.k, sK + ring.slot * kTile, w.b, w.hk, j * BN, w.keys, a.Nk,
+                                 tc::smem_u32(&sh.k_full[ring.slot]));
+                ++kfills;
+                if (j == 0) {
+                    if (n > 0 && !(ok = poll_bar(&sh.g_empty, (n - 1) & 1, abort_flag, err, (1 << 16) + 1))) break;
+                    load_tile<D>(maps.g, sG, w.b, w.h, w.qt * BM, tc::smem_u32(&sh.g_full));
+                    g_loaded = true;
+                    // the next item's rows on their way from HBM to L2
+                    QItem x = w;
+                    if (x.next(a) && x.T > 0) {
+                        prefetch_tile<D>(maps.q, x.b, x.h, x.qt * BM);
+                        prefetch_tile<D>(maps.g, x.b, x.h, x.qt * BM);
+                    }
+                }
+                if (vfills >= NS && !(ok = poll_bar(&sh.v_empty[ring.slot], ring.phase ^ 1, abort_flag, err, (3 << 16))))
+                    break;
+                load_key_tile<D>(maps.v, sV + ring.slot * kTile, w.b, w.hk, j * BN, w.keys, a.Nk,
+                                 tc::smem_u32(&sh.v_full[ring.slot]));
+                ++vfills;
+                ring.next(NS);
+            }
+            if (!ok) break;
+            ++n;
+        }
+        // gave up: let the copies in flight land before the CTA ends
+        if (!ok) {
+            if (q_loaded) tc::drain_bar(&sh.q_full, n & 1);
+            if (g_loaded) tc::drain_bar(&sh.g_full, n & 1);
+            for (uint32_t f = kfills > NS ? kfills - NS : 0; f < kfills; ++f)
+                tc::drain_bar(&sh.k_full[f % NS], (f / NS) & 1);
+            for (uint32_t f = vfills > NS ? vfills - NS : 0; f < vfills; ++f)
+                tc::drain_bar(&sh.v_full[f % NS], (f / NS) & 1);
+        }
+    } else if (warp == 9 && lane == 0) {
+        // ---------------------------------------------------------------- S MMA
+        Ring ring;
+        uint32_t n = 0, g = 0;
+        bool ok = true;
+        for (bool more = w.start(a); ok && more; more = w.next(a)) {
+            if (w.T == 0) continue;
+            if (!(ok = poll_bar(&sh.q_full, n & 1, abort_flag, err, (4 << 16)))) break;
+            for (int j = 0; j < w.T; ++j, ++g) {
+                const uint32_t b = g & 1;
+                if (!(ok = poll_bar(&sh.k_full[ring.slot], ring.phase, abort_flag, err, (5 << 16))) ||
+                    (g >= 2 && !(ok = poll_bar(&sh.s_free[b], ((g >> 1) & 1) ^ 1, abort_flag, err, (6 << 16)))))
+                    break;
+                tc::fence_after_sync();
+                mma_dot<D>(tmem + b * BN, sQ, sK + ring.slot * kTile);
+                tc::commit(tc::smem_u32(&sh.s_full[b]));
+                ring.next(NS);
+            }
+            if (!ok) break;
+            tc::commit(tc::smem_u32(&sh.q_empty));
+            ++n;
+        }
+        drain_mma(&sh.drain[0], &sh.keep_tmem, err, lost, 9 << 16);
+    } else if (warp == 10 && lane == 0) {
+        // ------------------------------------------------------- dP and dQ MMA
+        Ring kr, vr;
+        uint32_t n = 0, g = 0;
+        bool ok = true;
+        for (bool more = w.start(a); ok && more; more = w.next(a)) {
+            if (w.T == 0) continue;
+            if (!(ok = poll_bar(&sh.g_full, n & 1, abort_flag, err, (4 << 16) + 1))) break;
+            auto issue_dp = [&]() {
+                if (!(ok = poll_bar(&sh.v_full[vr.slot], vr.phase, abort_flag, err, (5 << 16) + 1))) return;
+                tc::fence_after_sync();
+                mma_dot<D>(tmem + 2 * BN, sG, sV + vr.slot * kTile);
+                tc::commit(tc::smem_u32(&sh.dp_full));
+                tc::commit(tc::smem_u32(&sh.v_empty[vr.slot]));
+                vr.next(NS);
+            };
+            issue_dp();
+            if (!ok) break;
+            // the first sum overwrites dQ: the last item's must be read out
+            if (n > 0 && !(ok = poll_bar(&sh.acc_free, (n - 1) & 1, abort_flag, err, (6 << 16) + 1))) break;
+            for (int j = 0; j < w.T; ++j, ++g) {
+                const uint32_t b = g & 1;
+                if (!(ok = poll_bar(&sh.ds_full, g & 1, abort_flag, err, (7 << 16)))) break;
+                // dS(j) written: dP(j) has been read too
+                if (j + 1 < w.T) {
+                    issue_dp();
+                    if (!ok) break;
+                } else {
+                    tc::commit(tc::smem_u32(&sh.g_empty));
+                }
+                tc::fence_after_sync();
+                const uint32_t tile = sK + kr.slot * kTile;   // (in shared memory since S(j))
+                mma_rows64<D>(tmem + 3 * BN, tmem + b * BN, tile, j > 0 ? 1u : 0u);
+                mma_rows64<D>(tmem + 3 * BN, tmem + b * BN + HN, tile + HN * 128, 1u);
+                tc::commit(tc::smem_u32(&sh.s_free[b]));
+                tc::commit(tc::smem_u32(&sh.k_empty[kr.slot]));
+                kr.next(NS);
+            }
+            if (!ok) break;
+            tc::commit(tc::smem_u32(&sh.acc_full));
+            ++n;
+        }
+        drain_mma(&sh.drain[1], &sh.keep_tmem, err, lost, (9 << 16) + 1);
+    } else if (warp < 8) {
+        // -------------------------------------------------------------- weights
+        const int h = warp >> 2, r = tid & 127;
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t tP = lane_base + 2 * BN + h * HN;
+        const float scale_log2 = a.scale * kLog2e;
+        const uint64_t xs2 = pack2(scale_log2, scale_log2);
+        uint32_t g = 0;
+        bool ok = true, more = w.start(a);
+        auto row_of = [&](const QItem& x) { return ((size_t)x.b * a.Hq + x.h) * a.Nq + (size_t)x.qt * BM + r; };
+        // this row's lse and delta, read an item ahead
+        float nl = 0.f, nd = 0.f;
+        if (more && w.qt * BM + r < a.Nq) {
+            nl = __ldg(a.lse + row_of(w));
+            nd = __ldg(a.delta + row_of(w));
+        }
+        for (; ok && more;) {
+            const float neg_lse = -nl * kLog2e, neg_delta = -nd;
+            QItem x = w;
+            const bool more_x = x.next(a);
+            nl = nd = 0.f;
+            if (more_x && x.qt * BM + r < a.Nq) {
+                nl = __ldg(a.lse + row_of(x));
+                nd = __ldg(a.delta + row_of(x));
+            }
+            const uint64_t nl2 = pack2(neg_lse, neg_lse), nd2 = pack2(neg_delta, neg_delta);
+            for (int j = 0; j < w.T; ++j, ++g) {
+                const uint32_t tS = lane_base + (g & 1) * BN + h * HN;
+                if (!(ok = warp_poll_bar(&sh.s_full[g & 1], (g >> 1) & 1, abort_flag, err, (11 << 16)))) break;
+                tc::fence_after_sync();
+                const int valid = w.keys - j * BN - h * HN;
+                if (valid < HN) mask_columns(tS, valid);   // past the keys: p = 0
+                uint32_t v[HN];
+                tc::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+                tc::tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < HN; e += 2) {
+                    fma2(v[e], v[e + 1], xs2, nl2, v[e], v[e + 1]);
+                    v[e] = __float_as_uint(tc::ex2(__uint_as_float(v[e])));
+                    v[e + 1] = __float_as_uint(tc::ex2(__uint_as_float(v[e + 1])));
+                }
+                if (!(ok = warp_poll_bar(&sh.dp_full, g & 1, abort_flag, err, (12 << 16)))) break;
+                tc::fence_after_sync();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t d[32], pk[16];
+                    tc::tmem_ld32(tP + q * 32, d);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const uint32_t* y = &v[q * 32 + e];
+                        const uint64_t s = mul2(sub2(d[e], d[e + 1], nd2), (uint64_t)y[0] | ((uint64_t)y[1] << 32));
+                        pk[e / 2] = bf16_pair(lo(s), hi(s));
+                    }
+                    tc::tmem_st16(tS + q * 16, pk);
+                }
+                tc::tmem_st_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.ds_full));
+            }
+            w = x;
+            more = more_x;
+        }
+    } else if (warp >= 12) {
+        // ------------------------------------------------------------- epilogue
+        const uint32_t tA = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 3 * BN;
+        const uint32_t area = sStage + (warp & 3) * 8192;
+        uint32_t n = 0, stores = 0;
+        for (bool more = w.start(a); more; more = w.next(a)) {
+            const int n0 = w.qt * BM + (warp & 3) * 32;
+            if (w.T > 0) {
+                if (!warp_poll_bar(&sh.acc_full, n & 1, abort_flag, err, (13 << 16))) break;
+                tc::fence_after_sync();
+                ++n;
+            }
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
+                uint32_t o[64];
+                if (w.T > 0) {
+                    tc::tmem_ld32(tA + c * 64, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
+                    tc::tmem_ld32(tA + c * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
+                    tc::tmem_ld_wait();
+                    if (c == D / 64 - 1) {
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.acc_free));
+                    }
+                }
+                uint32_t pk[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e)   // (no key: zeros)
+                    pk[e] = w.T > 0 ? bf16_pair(__uint_as_float(o[2 * e]) * a.scale, __uint_as_float(o[2 * e + 1]) * a.scale)
+                                    : 0u;
+                store_rows<1>(maps.dq, area + (stores++ & 1) * 4096, pk, c * 64, w.b, w.h, n0, n0 < a.Nq, lane);
+            }
+        }
+        if (lane == 0) tc::bulk_wait_read<0>();   // shared memory outlives its stores
+    }
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 9 && !sh.keep_tmem) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D>
+int launch_dkv(const CrossArgs& a, float* part, int* err, int* lost, cudaStream_t st) {
+    const void* fn = (const void*)cross_dkv_sm100_kernel<D>;
+    KvMaps m;
+    if (!make_tile_map(&m.q, a.Q, a.B, a.Hq, a.Nq, D, BM) || !make_tile_map(&m.g, a.dO, a.B, a.Hq, a.Nq, D, BM) ||
+        !make_tile_map(&m.k, a.K, a.B, a.Hkv, a.Nk, D, BM) || !make_tile_map(&m.v, a.V, a.B, a.Hkv, a.Nk, D, BM))
+        return SVGEAR_ERR_CUDA;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kv_smem<D>()) != cudaSuccess)
+        return SVGEAR_ERR_CUDA;
+    cross_dkv_sm100_kernel<D><<<kSms, kKvThreads, kv_smem<D>(), st>>>(m, a, part, err, lost);
+    count_launches(1);
+    SVGEAR_LAUNCH_CHECK();
+    return SVGEAR_OK;
+}
+
+template <int D>
+int launch_dq(const CrossArgs& a, int* err, int* lost, cudaStream_t st) {
+    const void* fn = (const void*)cross_dq_sm100_kernel<D>;
+    QMaps m;
+    if (!make_tile_map(&m.q, a.Q, a.B, a.Hq, a.Nq, D, BM) || !make_tile_map(&m.g, a.dO, a.B, a.Hq, a.Nq, D, BM) ||
+        !make_tile_map(&m.dq, a.dQ, a.B, a.Hq, a.Nq, D, 32) || !make_row_maps(&m.k, a.K, a.B, a.Hkv, a.Nk, D) ||
+        !make_row_maps(&m.v, a.V, a.B, a.Hkv, a.Nk, D))
+        return SVGEAR_ERR_CUDA;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)q_smem<D>()) != cudaSuccess)
+        return SVGEAR_ERR_CUDA;
+    const long long items = (long long)a.B * a.Hq * ceil_div(a.Nq, BM);
+    cross_dq_sm100_kernel<D><<<(int)(items < kSms ? items : kSms), kQThreads, q_smem<D>(), st>>>(m, a, err, lost);
+    count_launches(1);
+    SVGEAR_LAUNCH_CHECK();
+    return SVGEAR_OK;
+}
+
+}  // namespace
+}  // namespace crosstc
+
+int launch_cross_backward_sm100(const CrossArgs& a, float* part, int* err, cudaStream_t st) {
+    if (tmem_lost_latched()) return SVGEAR_ERR_TMEM_LOST;
+    int* lost = nullptr;
+    int s = tmem_lost_word(&lost);
+    if (s) return s;
+    s = a.D == 128 ? crosstc::launch_dq<128>(a, err, lost, st) : crosstc::launch_dq<64>(a, err, lost, st);
+    if (s) return s;
+    s = a.D == 128 ? crosstc::launch_dkv<128>(a, part, err, lost, st) : crosstc::launch_dkv<64>(a, part, err, lost, st);
+    if (s) return s;
+    return launch_cross_dkv_join(a, SVGEAR_BF16, crosstc::BM, kSms, part, st);
+}
+
+}  // namespace svgear

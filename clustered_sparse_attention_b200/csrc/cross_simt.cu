@@ -555,7 +555,13 @@ int dkv(const CrossArgs& a, int ctas, float* part, cudaStream_t st) {
     if (int s = set_smem(cross_dkv_kernel<T, D>, smem)) return s;
     cross_dkv_kernel<T, D><<<ctas, kThreads, smem, st>>>(a, part);
     count_launches(1);
-    cross_dkv_join_kernel<T, D, N><<<dim3(ceil_div(a.Nk, N), a.B * a.Hkv), 256, 0, st>>>(a, M, ctas, part);
+    SVGEAR_LAUNCH_CHECK();
+    return SVGEAR_OK;
+}
+template <typename T, int D>
+int dkv_join(const CrossArgs& a, int rows, int ctas, const float* part, cudaStream_t st) {
+    constexpr int BN = sizeof(T) == 4 ? kCrossSimtN : kCrossTcN;
+    cross_dkv_join_kernel<T, D, BN><<<dim3(ceil_div(a.Nk, BN), a.B * a.Hkv), 256, 0, st>>>(a, rows, ctas, part);
     count_launches(1);
     SVGEAR_LAUNCH_CHECK();
     return SVGEAR_OK;
@@ -581,11 +587,15 @@ int launch_cross_delta(const CrossArgs& a, int dtype, const HeldTokens* q, const
                        void* qx, cudaStream_t st) {
     return SVGEAR_PICK(delta, a, q, o, qx, st);
 }
-int launch_cross_dq_simt(const CrossArgs& a, int dtype, cudaStream_t st) {
-    return SVGEAR_PICK(dq, a, st);
+int launch_cross_dkv_join(const CrossArgs& a, int dtype, int rows, int ctas, const float* part,
+                          cudaStream_t st) {
+    return SVGEAR_PICK(dkv_join, a, rows, ctas, part, st);
 }
-int launch_cross_dkv_simt(const CrossArgs& a, int dtype, int ctas, float* part, cudaStream_t st) {
-    return SVGEAR_PICK(dkv, a, ctas, part, st);
+int launch_cross_backward_simt(const CrossArgs& a, int ctas, float* part, cudaStream_t st) {
+    int s = a.D == 128 ? dq<float, 128>(a, st) : dq<float, 64>(a, st);
+    if (s) return s;
+    if ((s = a.D == 128 ? dkv<float, 128>(a, ctas, part, st) : dkv<float, 64>(a, ctas, part, st))) return s;
+    return launch_cross_dkv_join(a, SVGEAR_F32, M, ctas, part, st);
 }
 
 }  // namespace svgear

@@ -463,7 +463,20 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
                 free_o();
             } else {
                 const int n0 = row - lane;
-                store_rows<D>(maps.o, sStage + warp * 4096, tO, inv, w.b, w.h, n0, n0 < a.Nq, lane, free_o);
+                uint32_t o[D];
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c)
+                    tc::tmem_ld32(tO + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[c * 32]));
+                tc::tmem_ld_wait();
+                free_o();
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        pk[e] = bf16_pair(__uint_as_float(o[c * 64 + 2 * e]) * inv, __uint_as_float(o[c * 64 + 2 * e + 1]) * inv);
+                    store_rows<0>(maps.o, sStage + warp * 4096, pk, c * 64, w.b, w.h, n0, n0 < a.Nq, lane);
+                }
             }
         }
         if (lane == 0) tc::bulk_wait_read<0>();   // shared memory outlives its stores

@@ -98,44 +98,27 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Writes 64 bf16 columns (32 packed words) of this thread's row to the warp's
-// 4 KB staging area (32 rows x 128 bytes, 128-byte swizzle).
-__device__ __forceinline__ void stage_row(uint32_t area, int lane, const uint32_t (&pk)[32]) {
+// Stores 64 bf16 columns [col0, col0 + 64) of 32 rows, one row per lane (packed
+// pairs pk), to rows n0.. of head (b, h): through a 4 KB staging area of the
+// warp (128-byte swizzle) and a TMA store, so that whole lines reach L2 (each
+// lane storing its own row would touch 32 lines per instruction).  A warp with
+// PENDING + 1 areas uses them in turn.  `map` has boxes of 32 rows; rows past
+// the tensor are left out.
+template <int PENDING>
+__device__ __forceinline__ void store_rows(const TileMap& map, uint32_t area, const uint32_t (&pk)[32], int col0,
+                                           int b, int h, int n0, bool any_row, int lane) {
+    if (lane == 0) tc::bulk_wait_read<PENDING>();   // this area's last store has been read
+    __syncwarp();
 #pragma unroll
     for (int c = 0; c < 8; ++c)
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(area + lane * 128 + ((c ^ (lane & 7)) << 4)),
                      "r"(pk[4 * c]), "r"(pk[4 * c + 1]), "r"(pk[4 * c + 2]), "r"(pk[4 * c + 3])
                      : "memory");
-}
-// Writes this thread's row of D fp32 values in tensor memory, times f and
-// rounded to bf16, to row n0 + lane of head (b, h): the warp's 32 rows go
-// through its staging area and a TMA store, so that whole lines reach L2
-// (each lane storing its own row would touch 32 lines per instruction).
-// `map` has boxes of 32 rows; rows past the tensor are left out.  read_done
-// runs once the TMEM columns are in registers.
-template <int D, typename F>
-__device__ __forceinline__ void store_rows(const TileMap& map, uint32_t area, uint32_t taddr, float f, int b,
-                                           int h, int n0, bool any_row, int lane, F read_done) {
-    uint32_t o[D];
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) tc::tmem_ld32(taddr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[c * 32]));
-    tc::tmem_ld_wait();
-    read_done();
-#pragma unroll
-    for (int g = 0; g < D / 64; ++g) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-            pk[e] = bf16_pair(__uint_as_float(o[g * 64 + 2 * e]) * f, __uint_as_float(o[g * 64 + 2 * e + 1]) * f);
-        if (lane == 0) tc::bulk_wait_read<0>();   // the area's last store has been read
-        __syncwarp();
-        stage_row(area, lane, pk);
-        tc::fence_async_smem();
-        __syncwarp();
-        if (lane == 0 && any_row) {
-            tc::tma_store_4d(&map.box, area, g * 64, n0, h * map.hmul, b * map.bmul);
-            tc::bulk_commit();
-        }
+    tc::fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        if (any_row) tc::tma_store_4d(&map.box, area, col0, n0, h * map.hmul, b * map.bmul);
+        tc::bulk_commit();
     }
 }
 
@@ -159,6 +142,17 @@ __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a_tmem, uint3
                                          uint32_t accumulate) {
     tc::mma_bf16_ts_k128(d_tmem, a_tmem, tc::sw128_desc(sX, 16384, 1024), tc::idesc_bf16(BM, D, true),
                          accumulate);
+}
+
+// The same over 64 rows of X.
+template <int D>
+__device__ __forceinline__ void mma_rows64(uint32_t d_tmem, uint32_t a_tmem, uint32_t sX,
+                                           uint32_t accumulate) {
+    constexpr uint32_t kIdesc = tc::idesc_bf16(BM, D, true);
+    const uint64_t desc = tc::sw128_desc(sX, 16384, 1024);
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+        tc::mma_bf16_ts(d_tmem, a_tmem + ks * 8, desc + ks * 128, kIdesc, ks > 0 ? 1u : accumulate);
 }
 
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
