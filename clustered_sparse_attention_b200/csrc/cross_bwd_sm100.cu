@@ -81,20 +81,25 @@ __device__ __forceinline__ void drain_mma(uint64_t* bar, int* keep_tmem, int* er
 // ---------------------------------------------------------------------------
 // dK, dV: a persistent CTA per SM takes an equal share of the iterations (key
 // tile, query head, query tile); see KvUnit.  K and V of the unit stay in
-// shared memory; Q and dO tiles stream through a ring, with lse and delta of
-// their rows.  Rows (TMEM lanes) are keys, columns queries:
+// shared memory; Q and dO tiles stream through a ring each, with lse and delta of
+// their rows in a third.  Rows (TMEM lanes) are keys, columns queries:
 //   chain A: S^T = K Q^T -> P^T (over S^T) -> dV += P^T dO
 //   chain B: dP^T = V dO^T -> dS^T (over dP^T) -> dK += dS^T Q
 // each issued by its own thread, so that S(i + 1) follows dV(i), dP(i + 1)
 // follows dK(i), and either runs beside the other chain's arithmetic.
 // TMEM: S | dP | dV | dK.
+// A copy takes some 2,000 cycles to arrive.  Q(i) is held from S(i) to dK(i), so
+// its ring has three slots where dO's has two: with two of both, S(i + 1) waited
+// for its Q in every iteration (4,300 cycles each against 2,048 of MMA work).
 // ---------------------------------------------------------------------------
 constexpr int kKvThreads = 12 * 32;   // 0-7 weights, 8 TMA, 9 and 10 MMA chains, 11 lse and delta
 
 template <int D>
-constexpr int kv_stages() { return D == 128 ? 2 : 4; }
+constexpr int kv_q_slots() { return D == 128 ? 3 : 4; }
 template <int D>
-constexpr uint32_t kv_smem() { return (2 + 2 * kv_stages<D>()) * (D / 64) * 16384 + 1024; }
+constexpr int kv_g_slots() { return D == 128 ? 2 : 4; }
+template <int D>
+constexpr uint32_t kv_smem() { return (2 + kv_q_slots<D>() + kv_g_slots<D>()) * (D / 64) * 16384; }
 
 struct KvMaps {
     TileMap q, g, k, v;
@@ -102,12 +107,13 @@ struct KvMaps {
 
 struct KvShared {
     uint64_t kv_full;
-    uint64_t full[4], empty[4];
+    uint64_t q_full[4], q_empty[4], g_full[4], g_empty[4];
+    uint64_t l_full[2], l_empty[2];
     uint64_t s_full, p_full, dp_full, ds_full;
     uint64_t acc_full, acc_free;
     uint64_t drain[2];
-    alignas(16) float neg_lse2[4][BM];   // -lse log2 e of the stage's rows
-    alignas(16) float neg_delta[4][BM];
+    alignas(16) float neg_lse2[2][BM];   // -lse log2 e of a query tile's rows
+    alignas(16) float neg_delta[2][BM];
     uint32_t tmem_base;
     int abort_flag;
     int keep_tmem;
@@ -142,20 +148,28 @@ __global__ void __launch_bounds__(kKvThreads, 1)
 cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* __restrict__ part,
                        int* __restrict__ err, int* __restrict__ lost) {
     constexpr uint32_t kTile = (D / 64) * 16384;
-    constexpr int NS = kv_stages<D>();
+    constexpr int NQ = kv_q_slots<D>(), NG = kv_g_slots<D>();
     if (tc::refuse_start(lost, err)) return;
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ KvShared sh;
-    const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t sK = base, sV = sK + kTile, sRing = sV + kTile;   // stage: Q, dO
+    const uint32_t base = tc::smem_u32(smem_raw);   // 1024-byte aligned: see launch_dkv()
+    const uint32_t sK = base, sV = sK + kTile, sQ = sV + kTile, sG = sQ + NQ * kTile;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t units = kv_total_units<BN>(a);
     if (tid == 0) {
         tc::mbar_init(tc::smem_u32(&sh.kv_full), 2);
-        for (int s = 0; s < NS; ++s) {
-            tc::mbar_init(tc::smem_u32(&sh.full[s]), 3);    // Q, dO, lse and delta
-            tc::mbar_init(tc::smem_u32(&sh.empty[s]), 2);   // both chains
+        for (int s = 0; s < NQ; ++s) {
+            tc::mbar_init(tc::smem_u32(&sh.q_full[s]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.q_empty[s]), 1);   // dK, which follows S
+        }
+        for (int s = 0; s < NG; ++s) {
+            tc::mbar_init(tc::smem_u32(&sh.g_full[s]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.g_empty[s]), 2);   // dV and dP
+        }
+        for (int s = 0; s < 2; ++s) {
+            tc::mbar_init(tc::smem_u32(&sh.l_full[s]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.l_empty[s]), 8);
         }
         tc::mbar_init(tc::smem_u32(&sh.s_full), 1);
         tc::mbar_init(tc::smem_u32(&sh.p_full), 8);
@@ -184,8 +198,8 @@ cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* 
 
     if (warp == 8 && lane == 0) {
         // ------------------------------------------------------------ producer
-        Ring ring;
-        uint32_t fills = 0, n = 0;
+        Ring qr, gr;
+        uint32_t qfills = 0, gfills = 0, n = 0;
         bool ok = true;
         while (ok && p.next(a)) {
             // the last unit's products have read K and V
@@ -195,119 +209,151 @@ cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* 
             ++n;
             int g = (int)(p.first / qtiles), qt = (int)(p.first - (int64_t)g * qtiles);
             for (int64_t x = p.first; x < p.last; ++x) {
-                if (fills >= NS && !(ok = poll_bar(&sh.empty[ring.slot], ring.phase ^ 1, abort_flag, err, (2 << 16))))
+                if (qfills >= NQ && !(ok = poll_bar(&sh.q_empty[qr.slot], qr.phase ^ 1, abort_flag, err, (2 << 16))))
                     break;
-                const uint32_t bar = tc::smem_u32(&sh.full[ring.slot]), dst = sRing + ring.slot * 2 * kTile;
-                load_tile<D>(maps.q, dst, p.k.b, p.k.h * a.G + g, qt * BM, bar);
-                load_tile<D>(maps.g, dst + kTile, p.k.b, p.k.h * a.G + g, qt * BM, bar);
-                ++fills;
-                ring.next(NS);
+                load_tile<D>(maps.q, sQ + qr.slot * kTile, p.k.b, p.k.h * a.G + g, qt * BM,
+                             tc::smem_u32(&sh.q_full[qr.slot]));
+                ++qfills;
+                qr.next(NQ);
+                if (gfills >= NG && !(ok = poll_bar(&sh.g_empty[gr.slot], gr.phase ^ 1, abort_flag, err, (2 << 16) + 1)))
+                    break;
+                load_tile<D>(maps.g, sG + gr.slot * kTile, p.k.b, p.k.h * a.G + g, qt * BM,
+                             tc::smem_u32(&sh.g_full[gr.slot]));
+                ++gfills;
+                gr.next(NG);
                 if (++qt == qtiles) {
                     qt = 0;
                     ++g;
                 }
             }
         }
-        // gave up: let the copies in flight land before the CTA ends (a stage
-        // whose lse never came is bounded by the clock)
+        // gave up: let the copies in flight land before the CTA ends
         if (!ok) {
             if (n > 0) tc::drain_bar(&sh.kv_full, (n - 1) & 1);
-            for (uint32_t f = fills > NS ? fills - NS : 0; f < fills; ++f)
-                tc::drain_bar(&sh.full[f % NS], (f / NS) & 1);
+            for (uint32_t f = qfills > NQ ? qfills - NQ : 0; f < qfills; ++f)
+                tc::drain_bar(&sh.q_full[f % NQ], (f / NQ) & 1);
+            for (uint32_t f = gfills > NG ? gfills - NG : 0; f < gfills; ++f)
+                tc::drain_bar(&sh.g_full[f % NG], (f / NG) & 1);
         }
     } else if (warp == 11) {
         // -------------------------------------------------------- lse and delta
-        Ring ring;
-        uint32_t fills = 0;
+        uint32_t i = 0;
         bool ok = true;
         while (ok && p.next(a)) {
             int g = (int)(p.first / qtiles), qt = (int)(p.first - (int64_t)g * qtiles);
-            for (int64_t x = p.first; x < p.last; ++x) {
+            for (int64_t x = p.first; x < p.last; ++x, ++i) {
                 const size_t r0 = ((size_t)p.k.b * a.Hq + p.k.h * a.G + g) * a.Nq + (size_t)qt * BM;
                 float l[4], d[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {   // rows past the end: p = e^{-inf} = 0
-                    const bool in = qt * BM + 32 * i + lane < a.Nq;
-                    l[i] = in ? __ldg(a.lse + r0 + 32 * i + lane) * -kLog2e : -INFINITY;
-                    d[i] = in ? -__ldg(a.delta + r0 + 32 * i + lane) : 0.f;
+                for (int c = 0; c < 4; ++c) {   // rows past the end: p = e^{-inf} = 0
+                    const bool in = qt * BM + 32 * c + lane < a.Nq;
+                    l[c] = in ? __ldg(a.lse + r0 + 32 * c + lane) * -kLog2e : -INFINITY;
+                    d[c] = in ? -__ldg(a.delta + r0 + 32 * c + lane) : 0.f;
                 }
-                if (fills >= NS &&
-                    !(ok = warp_poll_bar(&sh.empty[ring.slot], ring.phase ^ 1, abort_flag, err, (3 << 16))))
+                if (i >= 2 && !(ok = warp_poll_bar(&sh.l_empty[i & 1], ((i >> 1) - 1) & 1, abort_flag, err, (3 << 16))))
                     break;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    sh.neg_lse2[ring.slot][32 * i + lane] = l[i];
-                    sh.neg_delta[ring.slot][32 * i + lane] = d[i];
+                for (int c = 0; c < 4; ++c) {
+                    sh.neg_lse2[i & 1][32 * c + lane] = l[c];
+                    sh.neg_delta[i & 1][32 * c + lane] = d[c];
                 }
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.full[ring.slot]));
-                ++fills;
-                ring.next(NS);
+                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.l_full[i & 1]));
                 if (++qt == qtiles) {
                     qt = 0;
                     ++g;
                 }
             }
         }
-    } else if (warp >= 9 && lane == 0) {
-        // --------------------------------------------------- MMA chains A and B
-        const bool chain_a = warp == 9;
-        uint64_t* sc_full = chain_a ? &sh.s_full : &sh.dp_full;    // score tile written
-        uint64_t* w_full = chain_a ? &sh.p_full : &sh.ds_full;     // weights written over it
-        const uint32_t tW = tmem + (chain_a ? 0 : BN), tAcc = tmem + 2 * BN + (chain_a ? 0 : D);
-        const uint32_t sStat = chain_a ? sK : sV;
-        const uint32_t score_off = chain_a ? 0 : kTile;   // Q for S, dO for dP
-        const uint32_t acc_off = chain_a ? kTile : 0;     // dO for dV, Q for dK
-        Ring ring;
+    } else if (warp == 9 && lane == 0) {
+        // ------------------------------------------------ MMA chain A: S and dV
+        Ring qr, gr;
         uint32_t n = 0, i = 0;
         bool ok = true;
         while (ok && p.next(a)) {
+            auto issue_s = [&]() {
+                tc::fence_after_sync();
+                mma_dot<D>(tmem, sK, sQ + qr.slot * kTile);
+                tc::commit(tc::smem_u32(&sh.s_full));
+                qr.next(NQ);
+            };
             ok = poll_bar(&sh.kv_full, n & 1, abort_flag, err, (4 << 16)) &&
-                 poll_bar(&sh.full[ring.slot], ring.phase, abort_flag, err, (5 << 16));
+                 poll_bar(&sh.q_full[qr.slot], qr.phase, abort_flag, err, (5 << 16));
             if (!ok) break;
-            tc::fence_after_sync();
-            mma_dot<D>(tW, sStat, sRing + ring.slot * 2 * kTile + score_off);
-            tc::commit(tc::smem_u32(sc_full));
+            issue_s();
             // the first sum overwrites the accumulator: the last must be read out
             if (n > 0 && !(ok = poll_bar(&sh.acc_free, (n - 1) & 1, abort_flag, err, (6 << 16)))) break;
             for (int64_t x = p.first; x < p.last; ++x, ++i) {
-                const uint32_t cur = sRing + ring.slot * 2 * kTile;
-                uint64_t* cur_empty = &sh.empty[ring.slot];
-                ring.next(NS);
                 const bool more = x + 1 < p.last;
-                if (more && !(ok = poll_bar(&sh.full[ring.slot], ring.phase, abort_flag, err, (5 << 16)))) break;
-                if (!(ok = poll_bar(w_full, i & 1, abort_flag, err, (7 << 16)))) break;
+                if (!(ok = poll_bar(&sh.g_full[gr.slot], gr.phase, abort_flag, err, (5 << 16) + 1)) ||
+                    (more && !(ok = poll_bar(&sh.q_full[qr.slot], qr.phase, abort_flag, err, (5 << 16)))) ||
+                    !(ok = poll_bar(&sh.p_full, i & 1, abort_flag, err, (7 << 16))))
+                    break;
                 tc::fence_after_sync();
-                mma_rows64<D>(tAcc, tW, cur + acc_off, x > p.first ? 1u : 0u);
-                mma_rows64<D>(tAcc, tW + HN, cur + acc_off + HN * 128, 1u);
-                if (more) {
-                    mma_dot<D>(tW, sStat, sRing + ring.slot * 2 * kTile + score_off);
-                    tc::commit(tc::smem_u32(sc_full));
-                }
-                tc::commit(tc::smem_u32(cur_empty));
+                const uint32_t tile = sG + gr.slot * kTile;
+                mma_rows64<D>(tmem + 2 * BN, tmem, tile, x > p.first ? 1u : 0u);
+                mma_rows64<D>(tmem + 2 * BN, tmem + HN, tile + HN * 128, 1u);
+                if (more) issue_s();
+                tc::commit(tc::smem_u32(&sh.g_empty[gr.slot]));
+                gr.next(NG);
             }
             if (!ok) break;
             tc::commit(tc::smem_u32(&sh.acc_full));
             ++n;
         }
-        drain_mma(&sh.drain[chain_a ? 0 : 1], &sh.keep_tmem, err, lost, (9 << 16) + (chain_a ? 0 : 1));
+        drain_mma(&sh.drain[0], &sh.keep_tmem, err, lost, 9 << 16);
+    } else if (warp == 10 && lane == 0) {
+        // ----------------------------------------------- MMA chain B: dP and dK
+        Ring qr, gr;
+        uint32_t n = 0, i = 0;
+        bool ok = true;
+        while (ok && p.next(a)) {
+            auto issue_dp = [&]() {
+                tc::fence_after_sync();
+                mma_dot<D>(tmem + BN, sV, sG + gr.slot * kTile);
+                tc::commit(tc::smem_u32(&sh.dp_full));
+                tc::commit(tc::smem_u32(&sh.g_empty[gr.slot]));
+                gr.next(NG);
+            };
+            ok = poll_bar(&sh.kv_full, n & 1, abort_flag, err, (4 << 16) + 1) &&
+                 poll_bar(&sh.g_full[gr.slot], gr.phase, abort_flag, err, (5 << 16) + 2);
+            if (!ok) break;
+            issue_dp();
+            if (n > 0 && !(ok = poll_bar(&sh.acc_free, (n - 1) & 1, abort_flag, err, (6 << 16) + 1))) break;
+            for (int64_t x = p.first; x < p.last; ++x, ++i) {
+                const bool more = x + 1 < p.last;
+                if ((more && !(ok = poll_bar(&sh.g_full[gr.slot], gr.phase, abort_flag, err, (5 << 16) + 2))) ||
+                    !(ok = poll_bar(&sh.ds_full, i & 1, abort_flag, err, (8 << 16))))
+                    break;
+                tc::fence_after_sync();
+                const uint32_t tile = sQ + qr.slot * kTile;   // (in shared memory since S(i))
+                mma_rows64<D>(tmem + 2 * BN + D, tmem + BN, tile, x > p.first ? 1u : 0u);
+                mma_rows64<D>(tmem + 2 * BN + D, tmem + BN + HN, tile + HN * 128, 1u);
+                if (more) issue_dp();
+                tc::commit(tc::smem_u32(&sh.q_empty[qr.slot]));
+                qr.next(NQ);
+            }
+            if (!ok) break;
+            tc::commit(tc::smem_u32(&sh.acc_full));
+            ++n;
+        }
+        drain_mma(&sh.drain[1], &sh.keep_tmem, err, lost, (9 << 16) + 1);
     } else if (warp < 8) {
         // -------------------------------------------------------------- weights
         const int h = warp >> 2, r = tid & 127;
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t tS = lane_base + h * HN, tP = lane_base + BN + h * HN;
         const uint64_t xs2 = pack2(scale_log2, scale_log2);
-        Ring ring;
         uint32_t n = 0, i = 0;
         bool ok = true;
         while (ok && p.next(a)) {
             for (int64_t x = p.first; x < p.last; ++x, ++i) {
-                if (!(ok = warp_poll_bar(&sh.full[ring.slot], ring.phase, abort_flag, err, (10 << 16)) &&
+                if (!(ok = warp_poll_bar(&sh.l_full[i & 1], (i >> 1) & 1, abort_flag, err, (10 << 16)) &&
                            warp_poll_bar(&sh.s_full, i & 1, abort_flag, err, (11 << 16))))
                     break;
                 tc::fence_after_sync();
-                const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(&sh.neg_lse2[ring.slot][h * HN]);
-                const ulonglong2* nd = reinterpret_cast<const ulonglong2*>(&sh.neg_delta[ring.slot][h * HN]);
+                const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(&sh.neg_lse2[i & 1][h * HN]);
+                const ulonglong2* nd = reinterpret_cast<const ulonglong2*>(&sh.neg_delta[i & 1][h * HN]);
                 uint32_t v[HN];
                 tc::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
                 tc::tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
@@ -357,8 +403,10 @@ cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* 
                 tc::tmem_st_wait();
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.ds_full));
-                ring.next(NS);
+                if (lane == 0) {
+                    tc::mbar_arrive(tc::smem_u32(&sh.ds_full));
+                    tc::mbar_arrive(tc::smem_u32(&sh.l_empty[i & 1]));
+                }
             }
             if (!ok) break;
             // the unit's sums (or this CTA's part of them): warpgroup 0 writes
@@ -417,14 +465,18 @@ cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* 
 // ---------------------------------------------------------------------------
 constexpr int kQThreads = 16 * 32;   // 0-7 weights, 8 TMA, 9 S, 10 dP and dQ, 12-15 epilogue
 
+// K(j) is held from S(j) to dQ(j) and S(j + 2) follows dQ(j): its ring needs a
+// third slot for the copy of K(j + 2) to arrive in time.
 template <int D>
-constexpr int q_slots() { return D == 128 ? 2 : 4; }
+constexpr int q_k_slots() { return D == 128 ? 3 : 4; }
 template <int D>
-constexpr uint32_t q_smem() { return (2 + 2 * q_slots<D>()) * (D / 64) * 16384 + 4 * 8192 + 1024; }
+constexpr int q_v_slots() { return D == 128 ? 2 : 4; }
+template <int D>
+constexpr uint32_t q_smem() { return (2 + q_k_slots<D>() + q_v_slots<D>()) * (D / 64) * 16384 + 1024; }
 
 struct QMaps {
     RowMaps k, v;
-    TileMap q, g, dq;   // dq: boxes of 32 rows
+    TileMap q, g;
 };
 
 struct QShared {
@@ -479,13 +531,13 @@ __global__ void __launch_bounds__(kQThreads, 1)
 cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __restrict__ err,
                       int* __restrict__ lost) {
     constexpr uint32_t kTile = (D / 64) * 16384;
-    constexpr int NS = q_slots<D>();
+    constexpr int NK = q_k_slots<D>(), NV = q_v_slots<D>();
     if (tc::refuse_start(lost, err)) return;
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ QShared sh;
     const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t sQ = base, sG = sQ + kTile, sK = sG + kTile, sV = sK + NS * kTile, sStage = sV + NS * kTile;
+    const uint32_t sQ = base, sG = sQ + kTile, sK = sG + kTile, sV = sK + NK * kTile;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         uint64_t* one[] = {&sh.q_full, &sh.q_empty, &sh.g_full, &sh.g_empty, &sh.dp_full,
@@ -497,7 +549,7 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
             tc::mbar_init(tc::smem_u32(&sh.s_full[i]), 1);
             tc::mbar_init(tc::smem_u32(&sh.s_free[i]), 1);
         }
-        for (int i = 0; i < NS; ++i) {
+        for (int i = 0; i < 4; ++i) {
             tc::mbar_init(tc::smem_u32(&sh.k_full[i]), 1);
             tc::mbar_init(tc::smem_u32(&sh.k_empty[i]), 1);
             tc::mbar_init(tc::smem_u32(&sh.v_full[i]), 1);
@@ -520,7 +572,7 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
 
     if (warp == 8 && lane == 0) {
         // ------------------------------------------------------------ producer
-        Ring ring;
+        Ring kr, vr;
         uint32_t kfills = 0, vfills = 0, n = 0;
         bool ok = true, q_loaded = false, g_loaded = false;
         for (bool more = w.start(a); ok && more; more = w.next(a)) {
@@ -530,11 +582,12 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
             load_tile<D>(maps.q, sQ, w.b, w.h, w.qt * BM, tc::smem_u32(&sh.q_full));
             q_loaded = true;
             for (int j = 0; j < w.T; ++j) {
-                if (kfills >= NS && !(ok = poll_bar(&sh.k_empty[ring.slot], ring.phase ^ 1, abort_flag, err, (2 << 16))))
+                if (kfills >= NK && !(ok = poll_bar(&sh.k_empty[kr.slot], kr.phase ^ 1, abort_flag, err, (2 << 16))))
                     break;
-                load_key_tile<D>(maps.k, sK + ring.slot * kTile, w.b, w.hk, j * BN, w.keys, a.Nk,
-                                 tc::smem_u32(&sh.k_full[ring.slot]));
+                load_key_tile<D>(maps.k, sK + kr.slot * kTile, w.b, w.hk, j * BN, w.keys, a.Nk,
+                                 tc::smem_u32(&sh.k_full[kr.slot]));
                 ++kfills;
+                kr.next(NK);
                 if (j == 0) {
                     if (n > 0 && !(ok = poll_bar(&sh.g_empty, (n - 1) & 1, abort_flag, err, (1 << 16) + 1))) break;
                     load_tile<D>(maps.g, sG, w.b, w.h, w.qt * BM, tc::smem_u32(&sh.g_full));
@@ -546,12 +599,12 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
                         prefetch_tile<D>(maps.g, x.b, x.h, x.qt * BM);
                     }
                 }
-                if (vfills >= NS && !(ok = poll_bar(&sh.v_empty[ring.slot], ring.phase ^ 1, abort_flag, err, (3 << 16))))
+                if (vfills >= NV && !(ok = poll_bar(&sh.v_empty[vr.slot], vr.phase ^ 1, abort_flag, err, (3 << 16))))
                     break;
-                load_key_tile<D>(maps.v, sV + ring.slot * kTile, w.b, w.hk, j * BN, w.keys, a.Nk,
-                                 tc::smem_u32(&sh.v_full[ring.slot]));
+                load_key_tile<D>(maps.v, sV + vr.slot * kTile, w.b, w.hk, j * BN, w.keys, a.Nk,
+                                 tc::smem_u32(&sh.v_full[vr.slot]));
                 ++vfills;
-                ring.next(NS);
+                vr.next(NV);
             }
             if (!ok) break;
             ++n;
@@ -560,10 +613,10 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
         if (!ok) {
             if (q_loaded) tc::drain_bar(&sh.q_full, n & 1);
             if (g_loaded) tc::drain_bar(&sh.g_full, n & 1);
-            for (uint32_t f = kfills > NS ? kfills - NS : 0; f < kfills; ++f)
-                tc::drain_bar(&sh.k_full[f % NS], (f / NS) & 1);
-            for (uint32_t f = vfills > NS ? vfills - NS : 0; f < vfills; ++f)
-                tc::drain_bar(&sh.v_full[f % NS], (f / NS) & 1);
+            for (uint32_t f = kfills > NK ? kfills - NK : 0; f < kfills; ++f)
+                tc::drain_bar(&sh.k_full[f % NK], (f / NK) & 1);
+            for (uint32_t f = vfills > NV ? vfills - NV : 0; f < vfills; ++f)
+                tc::drain_bar(&sh.v_full[f % NV], (f / NV) & 1);
         }
     } else if (warp == 9 && lane == 0) {
         // ---------------------------------------------------------------- S MMA
@@ -581,7 +634,7 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
                 tc::fence_after_sync();
                 mma_dot<D>(tmem + b * BN, sQ, sK + ring.slot * kTile);
                 tc::commit(tc::smem_u32(&sh.s_full[b]));
-                ring.next(NS);
+                ring.next(NK);
             }
             if (!ok) break;
             tc::commit(tc::smem_u32(&sh.q_empty));
@@ -602,7 +655,7 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
                 mma_dot<D>(tmem + 2 * BN, sG, sV + vr.slot * kTile);
                 tc::commit(tc::smem_u32(&sh.dp_full));
                 tc::commit(tc::smem_u32(&sh.v_empty[vr.slot]));
-                vr.next(NS);
+                vr.next(NV);
             };
             issue_dp();
             if (!ok) break;
@@ -624,7 +677,7 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
                 mma_rows64<D>(tmem + 3 * BN, tmem + b * BN + HN, tile + HN * 128, 1u);
                 tc::commit(tc::smem_u32(&sh.s_free[b]));
                 tc::commit(tc::smem_u32(&sh.k_empty[kr.slot]));
-                kr.next(NS);
+                kr.next(NK);
             }
             if (!ok) break;
             tc::commit(tc::smem_u32(&sh.acc_full));
@@ -699,37 +752,38 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
     } else if (warp >= 12) {
         // ------------------------------------------------------------- epilogue
         const uint32_t tA = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 3 * BN;
-        const uint32_t area = sStage + (warp & 3) * 8192;
-        uint32_t n = 0, stores = 0;
+        uint32_t n = 0;
         for (bool more = w.start(a); more; more = w.next(a)) {
-            const int n0 = w.qt * BM + (warp & 3) * 32;
+            const int row = w.qt * BM + (warp & 3) * 32 + lane;
             if (w.T > 0) {
                 if (!warp_poll_bar(&sh.acc_full, n & 1, abort_flag, err, (13 << 16))) break;
                 tc::fence_after_sync();
                 ++n;
             }
-#pragma unroll 1
-            for (int c = 0; c < D / 64; ++c) {
-                uint32_t o[64];
-                if (w.T > 0) {
-                    tc::tmem_ld32(tA + c * 64, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
-                    tc::tmem_ld32(tA + c * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
-                    tc::tmem_ld_wait();
-                    if (c == D / 64 - 1) {
-                        tc::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.acc_free));
-                    }
-                }
-                uint32_t pk[32];
+            uint4* dst = reinterpret_cast<uint4*>(row_ptr<bf16>(a.dQ, w.b, w.h, row));
+            uint32_t pk[D / 2];
 #pragma unroll
-                for (int e = 0; e < 32; ++e)   // (no key: zeros)
-                    pk[e] = w.T > 0 ? bf16_pair(__uint_as_float(o[2 * e]) * a.scale, __uint_as_float(o[2 * e + 1]) * a.scale)
-                                    : 0u;
-                store_rows<1>(maps.dq, area + (stores++ & 1) * 4096, pk, c * 64, w.b, w.h, n0, n0 < a.Nq, lane);
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                if (w.T > 0) {
+                    tc::tmem_ld32(tA + c * 32, o);
+                    tc::tmem_ld_wait();
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e)   // (no key: zeros)
+                    pk[c * 16 + e] = w.T > 0 ? bf16_pair(__uint_as_float(o[2 * e]) * a.scale,
+                                                         __uint_as_float(o[2 * e + 1]) * a.scale)
+                                             : 0u;
             }
+            if (w.T > 0) {   // the accumulator has been read
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.acc_free));
+            }
+            if (row < a.Nq)
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
         }
-        if (lane == 0) tc::bulk_wait_read<0>();   // shared memory outlives its stores
     }
     __syncwarp();
     tc::fence_before_sync();
@@ -745,6 +799,11 @@ int launch_dkv(const CrossArgs& a, float* part, int* err, int* lost, cudaStream_
     if (!make_tile_map(&m.q, a.Q, a.B, a.Hq, a.Nq, D, BM) || !make_tile_map(&m.g, a.dO, a.B, a.Hq, a.Nq, D, BM) ||
         !make_tile_map(&m.k, a.K, a.B, a.Hkv, a.Nk, D, BM) || !make_tile_map(&m.v, a.V, a.B, a.Hkv, a.Nk, D, BM))
         return SVGEAR_ERR_CUDA;
+    // the swizzled tiles need 1024-byte alignment: the dynamic part starts after
+    // the static one, which is padded to a multiple of it
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, fn) != cudaSuccess) return SVGEAR_ERR_CUDA;
+    if (fa.sharedSizeBytes % 1024 != 0) return SVGEAR_ERR_UNSUPPORTED;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kv_smem<D>()) != cudaSuccess)
         return SVGEAR_ERR_CUDA;
     cross_dkv_sm100_kernel<D><<<kSms, kKvThreads, kv_smem<D>(), st>>>(m, a, part, err, lost);
@@ -758,7 +817,7 @@ int launch_dq(const CrossArgs& a, int* err, int* lost, cudaStream_t st) {
     const void* fn = (const void*)cross_dq_sm100_kernel<D>;
     QMaps m;
     if (!make_tile_map(&m.q, a.Q, a.B, a.Hq, a.Nq, D, BM) || !make_tile_map(&m.g, a.dO, a.B, a.Hq, a.Nq, D, BM) ||
-        !make_tile_map(&m.dq, a.dQ, a.B, a.Hq, a.Nq, D, 32) || !make_row_maps(&m.k, a.K, a.B, a.Hkv, a.Nk, D) ||
+        !make_row_maps(&m.k, a.K, a.B, a.Hkv, a.Nk, D) ||
         !make_row_maps(&m.v, a.V, a.B, a.Hkv, a.Nk, D))
         return SVGEAR_ERR_CUDA;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)q_smem<D>()) != cudaSuccess)

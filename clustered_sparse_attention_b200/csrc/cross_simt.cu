@@ -472,35 +472,64 @@ cross_dkv_join_kernel(CrossArgs a, int qrows, int ctas, const float* __restrict_
     }
 }
 
-// delta_i = do_i . o_i, one warp per row in fp32; o from its tensor or from
-// 8-bit codes, and with codes also q unpacked into qx [B][Hq][Nq][D].
+// delta_i = do_i . o_i in fp32, 16 bytes of the row per lane; o from its tensor
+// or from 8-bit codes, and with codes also q unpacked into qx [B][Hq][Nq][D].
+template <typename T>
+__device__ __forceinline__ void held_chunk(const HeldTokens& t, int64_t i, float* x) {
+    constexpr int C = Elem<T>::kPerChunk;
+    const float step = held_step(__ldg(t.exps + i / 32));
+    uint32_t w[C / 4];
+    if constexpr (C == 8) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(t.codes + i));
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+        w[0] = __ldg(reinterpret_cast<const uint32_t*>(t.codes + i));
+    }
+#pragma unroll
+    for (int e = 0; e < C; ++e) x[e] = (float)(int8_t)(w[e / 4] >> (8 * (e % 4))) * step;
+}
+__device__ __forceinline__ void store_chunk(float* p, const float* x) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store_chunk(__nv_bfloat16* p, const float* x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&b2);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 template <typename T, int D, bool HELD>
 __global__ void __launch_bounds__(256)
 cross_delta_kernel(CrossArgs a, HeldTokens qh, HeldTokens oh, T* __restrict__ qx) {
-    const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
-    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (r >= rows) return;
-    const int lane = threadIdx.x & 31;
-    constexpr int E = D / 32;   // elements per lane
-    const int64_t bh = r / a.Nq;
-    const int b = (int)(bh / a.Hq), h = (int)(bh - (int64_t)b * a.Hq);
-    const int64_t n = r - bh * a.Nq;
-    const T* g = row_ptr<const T>(a.dO, b, h, n) + E * lane;
+    constexpr int C = Elem<T>::kPerChunk, LR = D / C;   // lanes per row: 8, 16 or 32
+    const uint32_t rows = (uint32_t)((int64_t)a.B * a.Hq * a.Nq);
+    const uint64_t r64 = ((uint64_t)blockIdx.x * 256 + threadIdx.x) / LR;
+    const bool in = r64 < rows;
+    const uint32_t r = in ? (uint32_t)r64 : rows - 1;
+    const int c = (threadIdx.x % LR) * C;
+    const uint32_t bh = r / (uint32_t)a.Nq, n = r - bh * (uint32_t)a.Nq;
+    const int b = (int)(bh / (uint32_t)a.Hq), h = (int)(bh - (uint32_t)b * (uint32_t)a.Hq);
+    float g[C], o[C];
+    Elem<T>::load(row_ptr<const T>(a.dO, b, h, n) + c, g);
+    if (HELD) {
+        const int64_t i = (int64_t)r * D + c;
+        held_chunk<T>(oh, i, o);
+        float q[C];
+        held_chunk<T>(qh, i, q);
+        if (in) store_chunk(qx + i, q);
+    } else {
+        Elem<T>::load(row_ptr<const T>(a.O, b, h, n) + c, o);
+    }
     float s = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        float o;
-        if (HELD) {
-            const int64_t i = r * D + E * lane + e;
-            o = (float)oh.codes[i] * held_step(oh.exps[i / 32]);
-            qx[i] = Elem<T>::to((float)qh.codes[i] * held_step(qh.exps[i / 32]));
-        } else {
-            o = Elem<T>::from(row_ptr<const T>(a.O, b, h, n)[E * lane + e]);
-        }
-        s = fmaf(Elem<T>::from(g[e]), o, s);
-    }
-    s = warp_sum(s);
-    if (lane == 0) a.delta[r] = s;
+    for (int e = 0; e < C; ++e) s = fmaf(g[e], o[e], s);
+#pragma unroll
+    for (int x = LR / 2; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+    if (in && c == 0) a.delta[r] = s;
 }
 
 template <typename F>
@@ -531,7 +560,7 @@ int join(const CrossArgs& a, int splits, const float* o_part, const float* lse_p
 }
 template <typename T, int D>
 int delta(const CrossArgs& a, const HeldTokens* q, const HeldTokens* o, void* qx, cudaStream_t st) {
-    const int grid = ceil_div((long long)a.B * a.Hq * a.Nq, 8);
+    const int grid = ceil_div((long long)a.B * a.Hq * a.Nq * (D / Elem<T>::kPerChunk), 256);
     if (q)
         cross_delta_kernel<T, D, true><<<grid, 256, 0, st>>>(a, *q, *o, static_cast<T*>(qx));
     else
