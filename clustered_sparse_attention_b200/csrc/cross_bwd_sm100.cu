@@ -83,16 +83,18 @@ __device__ __forceinline__ void drain_mma(uint64_t* bar, int* keep_tmem, int* er
 // tile, query head, query tile); see KvUnit.  K and V of the unit stay in
 // shared memory; Q and dO tiles stream through a ring each, with lse and delta of
 // their rows in a third.  Rows (TMEM lanes) are keys, columns queries:
-//   chain A: S^T = K Q^T -> P^T (over S^T) -> dV += P^T dO
-//   chain B: dP^T = V dO^T -> dS^T (over dP^T) -> dK += dS^T Q
-// each issued by its own thread, so that S(i + 1) follows dV(i), dP(i + 1)
-// follows dK(i), and either runs beside the other chain's arithmetic.
+//   S^T = K Q^T -> P^T (over S^T) -> dV += P^T dO
+//   dP^T = V dO^T -> dS^T (over dP^T) -> dK += dS^T Q
+// One thread issues dV(i), S(i + 1), dK(i), dP(i + 1) in this order, so that the
+// weights of i + 1 are computed beside dK(i) and dP(i + 1).  (With a thread for
+// either chain the four products ran interleaved, S(i + 1) came as late as
+// dP(i + 1) and the weights had the tensor pipe idle: 4,000 cycles an iteration.)
 // TMEM: S | dP | dV | dK.
 // A copy takes some 2,000 cycles to arrive.  Q(i) is held from S(i) to dK(i), so
 // its ring has three slots where dO's has two: with two of both, S(i + 1) waited
 // for its Q in every iteration (4,300 cycles each against 2,048 of MMA work).
 // ---------------------------------------------------------------------------
-constexpr int kKvThreads = 12 * 32;   // 0-7 weights, 8 TMA, 9 and 10 MMA chains, 11 lse and delta
+constexpr int kKvThreads = 12 * 32;   // 0-7 weights, 8 TMA, 9 MMA, 11 lse and delta
 
 template <int D>
 constexpr int kv_q_slots() { return D == 128 ? 3 : 4; }
@@ -111,7 +113,7 @@ struct KvShared {
     uint64_t l_full[2], l_empty[2];
     uint64_t s_full, p_full, dp_full, ds_full;
     uint64_t acc_full, acc_free;
-    uint64_t drain[2];
+    uint64_t drain;
     alignas(16) float neg_lse2[2][BM];   // -lse log2 e of a query tile's rows
     alignas(16) float neg_delta[2][BM];
     uint32_t tmem_base;
@@ -165,7 +167,7 @@ cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* 
         }
         for (int s = 0; s < NG; ++s) {
             tc::mbar_init(tc::smem_u32(&sh.g_full[s]), 1);
-            tc::mbar_init(tc::smem_u32(&sh.g_empty[s]), 2);   // dV and dP
+            tc::mbar_init(tc::smem_u32(&sh.g_empty[s]), 1);   // dV, which follows dP
         }
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(tc::smem_u32(&sh.l_full[s]), 1);
@@ -175,10 +177,9 @@ cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* 
         tc::mbar_init(tc::smem_u32(&sh.p_full), 8);
         tc::mbar_init(tc::smem_u32(&sh.dp_full), 1);
         tc::mbar_init(tc::smem_u32(&sh.ds_full), 8);
-        tc::mbar_init(tc::smem_u32(&sh.acc_full), 2);
+        tc::mbar_init(tc::smem_u32(&sh.acc_full), 1);
         tc::mbar_init(tc::smem_u32(&sh.acc_free), 8);
-        tc::mbar_init(tc::smem_u32(&sh.drain[0]), 1);
-        tc::mbar_init(tc::smem_u32(&sh.drain[1]), 1);
+        tc::mbar_init(tc::smem_u32(&sh.drain), 1);
         sh.abort_flag = 0;
         sh.keep_tmem = 0;
         tc::mbar_init_fence();
@@ -266,78 +267,57 @@ cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* 
             }
         }
     } else if (warp == 9 && lane == 0) {
-        // ------------------------------------------------ MMA chain A: S and dV
-        Ring qr, gr;
+        // ------------------------------------------------------------ MMA issue
+        Ring qs, gs;   // Q of the next S, dO of the next dP
+        Ring qk, gv;   // Q of the next dK, dO of the next dV
         uint32_t n = 0, i = 0;
         bool ok = true;
+        auto issue_s = [&]() {
+            mma_dot<D>(tmem, sK, sQ + qs.slot * kTile);
+            tc::commit(tc::smem_u32(&sh.s_full));
+            qs.next(NQ);
+        };
+        auto issue_dp = [&]() {
+            mma_dot<D>(tmem + BN, sV, sG + gs.slot * kTile);
+            tc::commit(tc::smem_u32(&sh.dp_full));
+            gs.next(NG);
+        };
         while (ok && p.next(a)) {
-            auto issue_s = [&]() {
-                tc::fence_after_sync();
-                mma_dot<D>(tmem, sK, sQ + qr.slot * kTile);
-                tc::commit(tc::smem_u32(&sh.s_full));
-                qr.next(NQ);
-            };
             ok = poll_bar(&sh.kv_full, n & 1, abort_flag, err, (4 << 16)) &&
-                 poll_bar(&sh.q_full[qr.slot], qr.phase, abort_flag, err, (5 << 16));
+                 poll_bar(&sh.q_full[qs.slot], qs.phase, abort_flag, err, (5 << 16)) &&
+                 poll_bar(&sh.g_full[gs.slot], gs.phase, abort_flag, err, (5 << 16) + 1);
             if (!ok) break;
+            tc::fence_after_sync();
             issue_s();
-            // the first sum overwrites the accumulator: the last must be read out
+            issue_dp();
+            // the first sums overwrite the accumulators: the last must be read out
             if (n > 0 && !(ok = poll_bar(&sh.acc_free, (n - 1) & 1, abort_flag, err, (6 << 16)))) break;
             for (int64_t x = p.first; x < p.last; ++x, ++i) {
                 const bool more = x + 1 < p.last;
-                if (!(ok = poll_bar(&sh.g_full[gr.slot], gr.phase, abort_flag, err, (5 << 16) + 1)) ||
-                    (more && !(ok = poll_bar(&sh.q_full[qr.slot], qr.phase, abort_flag, err, (5 << 16)))) ||
+                const uint32_t acc = x > p.first ? 1u : 0u;
+                if ((more && !(ok = poll_bar(&sh.q_full[qs.slot], qs.phase, abort_flag, err, (5 << 16)))) ||
                     !(ok = poll_bar(&sh.p_full, i & 1, abort_flag, err, (7 << 16))))
                     break;
                 tc::fence_after_sync();
-                const uint32_t tile = sG + gr.slot * kTile;
-                mma_rows64<D>(tmem + 2 * BN, tmem, tile, x > p.first ? 1u : 0u);
-                mma_rows64<D>(tmem + 2 * BN, tmem + HN, tile + HN * 128, 1u);
+                const uint32_t g = sG + gv.slot * kTile, q = sQ + qk.slot * kTile;
+                mma_rows_2x64<D>(tmem + 2 * BN, tmem, g, acc);
                 if (more) issue_s();
-                tc::commit(tc::smem_u32(&sh.g_empty[gr.slot]));
-                gr.next(NG);
-            }
-            if (!ok) break;
-            tc::commit(tc::smem_u32(&sh.acc_full));
-            ++n;
-        }
-        drain_mma(&sh.drain[0], &sh.keep_tmem, err, lost, 9 << 16);
-    } else if (warp == 10 && lane == 0) {
-        // ----------------------------------------------- MMA chain B: dP and dK
-        Ring qr, gr;
-        uint32_t n = 0, i = 0;
-        bool ok = true;
-        while (ok && p.next(a)) {
-            auto issue_dp = [&]() {
-                tc::fence_after_sync();
-                mma_dot<D>(tmem + BN, sV, sG + gr.slot * kTile);
-                tc::commit(tc::smem_u32(&sh.dp_full));
-                tc::commit(tc::smem_u32(&sh.g_empty[gr.slot]));
-                gr.next(NG);
-            };
-            ok = poll_bar(&sh.kv_full, n & 1, abort_flag, err, (4 << 16) + 1) &&
-                 poll_bar(&sh.g_full[gr.slot], gr.phase, abort_flag, err, (5 << 16) + 2);
-            if (!ok) break;
-            issue_dp();
-            if (n > 0 && !(ok = poll_bar(&sh.acc_free, (n - 1) & 1, abort_flag, err, (6 << 16) + 1))) break;
-            for (int64_t x = p.first; x < p.last; ++x, ++i) {
-                const bool more = x + 1 < p.last;
-                if ((more && !(ok = poll_bar(&sh.g_full[gr.slot], gr.phase, abort_flag, err, (5 << 16) + 2))) ||
+                tc::commit(tc::smem_u32(&sh.g_empty[gv.slot]));   // dV(i), and dP(i) long before
+                gv.next(NG);
+                if ((more && !(ok = poll_bar(&sh.g_full[gs.slot], gs.phase, abort_flag, err, (5 << 16) + 1))) ||
                     !(ok = poll_bar(&sh.ds_full, i & 1, abort_flag, err, (8 << 16))))
                     break;
                 tc::fence_after_sync();
-                const uint32_t tile = sQ + qr.slot * kTile;   // (in shared memory since S(i))
-                mma_rows64<D>(tmem + 2 * BN + D, tmem + BN, tile, x > p.first ? 1u : 0u);
-                mma_rows64<D>(tmem + 2 * BN + D, tmem + BN + HN, tile + HN * 128, 1u);
+                mma_rows_2x64<D>(tmem + 2 * BN + D, tmem + BN, q, acc);
                 if (more) issue_dp();
-                tc::commit(tc::smem_u32(&sh.q_empty[qr.slot]));
-                qr.next(NQ);
+                tc::commit(tc::smem_u32(&sh.q_empty[qk.slot]));
+                qk.next(NQ);
             }
             if (!ok) break;
             tc::commit(tc::smem_u32(&sh.acc_full));
             ++n;
         }
-        drain_mma(&sh.drain[1], &sh.keep_tmem, err, lost, (9 << 16) + 1);
+        drain_mma(&sh.drain, &sh.keep_tmem, err, lost, 9 << 16);
     } else if (warp < 8) {
         // -------------------------------------------------------------- weights
         const int h = warp >> 2, r = tid & 127;
@@ -458,15 +438,21 @@ cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* 
 // dQ: an item is 128 query rows of one head; a persistent CTA per SM takes
 // items in turn.  Q and dO of the item stay in shared memory, K and V tiles
 // stream through two rings.  Rows (TMEM lanes) are queries, columns keys:
-//   S = Q K^T (two buffers), dP = dO V^T, dS = p (dP - delta) over S, dQ += dS K.
-// One thread issues dP(j + 1) and then dQ(j) when dS(j) is written, another
-// S(j + 2) when dQ(j) has read dS(j) out of its buffer, so the weights of j + 1
-// are computed meanwhile.  TMEM: S[0] | S[1] | dP | dQ.
+//   S = Q K^T, dP = dO V^T (two buffers), dS = p (dP - delta) over dP,
+//   dQ += dS K.
+// S(g + 1) is issued as soon as the weights have read S(g) into registers, dP(g + 2)
+// when dQ(g) has read dS(g), so that neither follows the weights of its own tile:
+// over the tiles of all items, the arithmetic of g runs beside the products of
+// g - 1 and g + 1.  Each product has its own issuing thread: a barrier test costs
+// its thread 100 to 300 cycles, a commit 65, and one thread for all three took
+// 3,400 cycles per tile for 1,536 of MMA work.  (With S in two buffers and dS over S, S(g + 2) came behind
+// dP(g + 1) and dQ(g) and the weights waited for it: 2,800 cycles per tile.)
+// TMEM: S | dP[0] | dP[1] | dQ.
 // ---------------------------------------------------------------------------
-constexpr int kQThreads = 16 * 32;   // 0-7 weights, 8 TMA, 9 S, 10 dP and dQ, 12-15 epilogue
+constexpr int kQThreads = 16 * 32;   // 0-7 weights, 8 TMA, 9-11 MMA, 12-15 epilogue
 
-// K(j) is held from S(j) to dQ(j) and S(j + 2) follows dQ(j): its ring needs a
-// third slot for the copy of K(j + 2) to arrive in time.
+// K(g) is held from S(g) to dQ(g): its ring needs a third slot for the copy of
+// K(g + 2) to arrive in time.
 template <int D>
 constexpr int q_k_slots() { return D == 128 ? 3 : 4; }
 template <int D>
@@ -482,10 +468,10 @@ struct QMaps {
 struct QShared {
     uint64_t q_full, q_empty, g_full, g_empty;
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-    uint64_t s_full[2], s_free[2];
-    uint64_t dp_full, ds_full;
+    uint64_t s_full, s_read;
+    uint64_t dp_full[2], ds_full[2], dq_done[2];
     uint64_t acc_full, acc_free;
-    uint64_t drain[2];
+    uint64_t drain[3];
     uint32_t tmem_base;
     int abort_flag;
     int keep_tmem;
@@ -540,15 +526,14 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
     const uint32_t sQ = base, sG = sQ + kTile, sK = sG + kTile, sV = sK + NK * kTile;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        uint64_t* one[] = {&sh.q_full, &sh.q_empty, &sh.g_full, &sh.g_empty, &sh.dp_full,
-                           &sh.acc_full, &sh.drain[0], &sh.drain[1]};
+        uint64_t* one[] = {&sh.q_full, &sh.q_empty, &sh.g_full, &sh.g_empty, &sh.s_full,
+                           &sh.dp_full[0], &sh.dp_full[1], &sh.dq_done[0], &sh.dq_done[1],
+                           &sh.acc_full, &sh.drain[0], &sh.drain[1], &sh.drain[2]};
         for (uint64_t* x : one) tc::mbar_init(tc::smem_u32(x), 1);
-        tc::mbar_init(tc::smem_u32(&sh.ds_full), 8);
+        tc::mbar_init(tc::smem_u32(&sh.s_read), 8);
+        tc::mbar_init(tc::smem_u32(&sh.ds_full[0]), 8);
+        tc::mbar_init(tc::smem_u32(&sh.ds_full[1]), 8);
         tc::mbar_init(tc::smem_u32(&sh.acc_free), 4);
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(tc::smem_u32(&sh.s_full[i]), 1);
-            tc::mbar_init(tc::smem_u32(&sh.s_free[i]), 1);
-        }
         for (int i = 0; i < 4; ++i) {
             tc::mbar_init(tc::smem_u32(&sh.k_full[i]), 1);
             tc::mbar_init(tc::smem_u32(&sh.k_empty[i]), 1);
@@ -618,77 +603,65 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
             for (uint32_t f = vfills > NV ? vfills - NV : 0; f < vfills; ++f)
                 tc::drain_bar(&sh.v_full[f % NV], (f / NV) & 1);
         }
-    } else if (warp == 9 && lane == 0) {
-        // ---------------------------------------------------------------- S MMA
+    } else if (warp >= 9 && warp < 12 && lane == 0) {
+        // ----------------------------------------- MMA issue: S, dP or dQ
+        const int role = warp - 9;
         Ring ring;
         uint32_t n = 0, g = 0;
         bool ok = true;
         for (bool more = w.start(a); ok && more; more = w.next(a)) {
             if (w.T == 0) continue;
-            if (!(ok = poll_bar(&sh.q_full, n & 1, abort_flag, err, (4 << 16)))) break;
-            for (int j = 0; j < w.T; ++j, ++g) {
-                const uint32_t b = g & 1;
-                if (!(ok = poll_bar(&sh.k_full[ring.slot], ring.phase, abort_flag, err, (5 << 16))) ||
-                    (g >= 2 && !(ok = poll_bar(&sh.s_free[b], ((g >> 1) & 1) ^ 1, abort_flag, err, (6 << 16)))))
-                    break;
-                tc::fence_after_sync();
-                mma_dot<D>(tmem + b * BN, sQ, sK + ring.slot * kTile);
-                tc::commit(tc::smem_u32(&sh.s_full[b]));
-                ring.next(NK);
-            }
-            if (!ok) break;
-            tc::commit(tc::smem_u32(&sh.q_empty));
-            ++n;
-        }
-        drain_mma(&sh.drain[0], &sh.keep_tmem, err, lost, 9 << 16);
-    } else if (warp == 10 && lane == 0) {
-        // ------------------------------------------------------- dP and dQ MMA
-        Ring kr, vr;
-        uint32_t n = 0, g = 0;
-        bool ok = true;
-        for (bool more = w.start(a); ok && more; more = w.next(a)) {
-            if (w.T == 0) continue;
-            if (!(ok = poll_bar(&sh.g_full, n & 1, abort_flag, err, (4 << 16) + 1))) break;
-            auto issue_dp = [&]() {
-                if (!(ok = poll_bar(&sh.v_full[vr.slot], vr.phase, abort_flag, err, (5 << 16) + 1))) return;
-                tc::fence_after_sync();
-                mma_dot<D>(tmem + 2 * BN, sG, sV + vr.slot * kTile);
-                tc::commit(tc::smem_u32(&sh.dp_full));
-                tc::commit(tc::smem_u32(&sh.v_empty[vr.slot]));
-                vr.next(NV);
-            };
-            issue_dp();
-            if (!ok) break;
-            // the first sum overwrites dQ: the last item's must be read out
-            if (n > 0 && !(ok = poll_bar(&sh.acc_free, (n - 1) & 1, abort_flag, err, (6 << 16) + 1))) break;
-            for (int j = 0; j < w.T; ++j, ++g) {
-                const uint32_t b = g & 1;
-                if (!(ok = poll_bar(&sh.ds_full, g & 1, abort_flag, err, (7 << 16)))) break;
-                // dS(j) written: dP(j) has been read too
-                if (j + 1 < w.T) {
-                    issue_dp();
-                    if (!ok) break;
-                } else {
-                    tc::commit(tc::smem_u32(&sh.g_empty));
+            // the item's Q, its dO, or dQ of the last item read out
+            ok = role == 0   ? poll_bar(&sh.q_full, n & 1, abort_flag, err, (4 << 16))
+                 : role == 1 ? poll_bar(&sh.g_full, n & 1, abort_flag, err, (4 << 16) + 1)
+                             : n == 0 || poll_bar(&sh.acc_free, (n - 1) & 1, abort_flag, err, (4 << 16) + 2);
+            if (role == 0) {
+                for (int j = 0; ok && j < w.T; ++j, ++g) {
+                    // S(g) overwrites S(g - 1), which must be in registers
+                    if (!(ok = poll_bar(&sh.k_full[ring.slot], ring.phase, abort_flag, err, (5 << 16)) &&
+                               (g == 0 || poll_bar(&sh.s_read, (g - 1) & 1, abort_flag, err, (6 << 16)))))
+                        break;
+                    tc::fence_after_sync();
+                    mma_dot<D>(tmem, sQ, sK + ring.slot * kTile);
+                    tc::commit(tc::smem_u32(&sh.s_full));
+                    ring.next(NK);
                 }
-                tc::fence_after_sync();
-                const uint32_t tile = sK + kr.slot * kTile;   // (in shared memory since S(j))
-                mma_rows64<D>(tmem + 3 * BN, tmem + b * BN, tile, j > 0 ? 1u : 0u);
-                mma_rows64<D>(tmem + 3 * BN, tmem + b * BN + HN, tile + HN * 128, 1u);
-                tc::commit(tc::smem_u32(&sh.s_free[b]));
-                tc::commit(tc::smem_u32(&sh.k_empty[kr.slot]));
-                kr.next(NK);
+                if (ok) tc::commit(tc::smem_u32(&sh.q_empty));
+            } else if (role == 1) {
+                for (int j = 0; ok && j < w.T; ++j, ++g) {
+                    // dP(g) overwrites dS(g - 2), which dQ must have read
+                    const uint32_t b = g & 1;
+                    if (!(ok = poll_bar(&sh.v_full[ring.slot], ring.phase, abort_flag, err, (5 << 16) + 1) &&
+                               (g < 2 || poll_bar(&sh.dq_done[b], ((g >> 1) & 1) ^ 1, abort_flag, err, (6 << 16) + 1))))
+                        break;
+                    tc::fence_after_sync();
+                    mma_dot<D>(tmem + BN + b * BN, sG, sV + ring.slot * kTile);
+                    tc::commit(tc::smem_u32(&sh.dp_full[b]));
+                    tc::commit(tc::smem_u32(&sh.v_empty[ring.slot]));
+                    ring.next(NV);
+                }
+                if (ok) tc::commit(tc::smem_u32(&sh.g_empty));
+            } else {
+                for (int j = 0; ok && j < w.T; ++j, ++g) {
+                    const uint32_t b = g & 1;
+                    if (!(ok = poll_bar(&sh.ds_full[b], (g >> 1) & 1, abort_flag, err, (7 << 16)))) break;
+                    tc::fence_after_sync();
+                    // (K(g) is in shared memory since S(g))
+                    mma_rows_2x64<D>(tmem + 3 * BN, tmem + BN + b * BN, sK + ring.slot * kTile, j > 0 ? 1u : 0u);
+                    tc::commit(tc::smem_u32(&sh.k_empty[ring.slot]));
+                    tc::commit(tc::smem_u32(&sh.dq_done[b]));
+                    ring.next(NK);
+                }
+                if (ok) tc::commit(tc::smem_u32(&sh.acc_full));
             }
-            if (!ok) break;
-            tc::commit(tc::smem_u32(&sh.acc_full));
             ++n;
         }
-        drain_mma(&sh.drain[1], &sh.keep_tmem, err, lost, (9 << 16) + 1);
+        drain_mma(&sh.drain[role], &sh.keep_tmem, err, lost, (9 << 16) + role);
     } else if (warp < 8) {
         // -------------------------------------------------------------- weights
         const int h = warp >> 2, r = tid & 127;
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t tP = lane_base + 2 * BN + h * HN;
+        const uint32_t tS = lane_base + h * HN;
         const float scale_log2 = a.scale * kLog2e;
         const uint64_t xs2 = pack2(scale_log2, scale_log2);
         uint32_t g = 0;
@@ -711,8 +684,8 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
             }
             const uint64_t nl2 = pack2(neg_lse, neg_lse), nd2 = pack2(neg_delta, neg_delta);
             for (int j = 0; j < w.T; ++j, ++g) {
-                const uint32_t tS = lane_base + (g & 1) * BN + h * HN;
-                if (!(ok = warp_poll_bar(&sh.s_full[g & 1], (g >> 1) & 1, abort_flag, err, (11 << 16)))) break;
+                const uint32_t b = g & 1, tP = tS + BN + b * BN;
+                if (!(ok = warp_poll_bar(&sh.s_full, g & 1, abort_flag, err, (11 << 16)))) break;
                 tc::fence_after_sync();
                 const int valid = w.keys - j * BN - h * HN;
                 if (valid < HN) mask_columns(tS, valid);   // past the keys: p = 0
@@ -720,13 +693,16 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
                 tc::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
                 tc::tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
                 tc::tmem_ld_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.s_read));
 #pragma unroll
                 for (int e = 0; e < HN; e += 2) {
                     fma2(v[e], v[e + 1], xs2, nl2, v[e], v[e + 1]);
                     v[e] = __float_as_uint(tc::ex2(__uint_as_float(v[e])));
                     v[e + 1] = __float_as_uint(tc::ex2(__uint_as_float(v[e + 1])));
                 }
-                if (!(ok = warp_poll_bar(&sh.dp_full, g & 1, abort_flag, err, (12 << 16)))) break;
+                if (!(ok = warp_poll_bar(&sh.dp_full[b], (g >> 1) & 1, abort_flag, err, (12 << 16)))) break;
                 tc::fence_after_sync();
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -739,12 +715,12 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
                         const uint64_t s = mul2(sub2(d[e], d[e + 1], nd2), (uint64_t)y[0] | ((uint64_t)y[1] << 32));
                         pk[e / 2] = bf16_pair(lo(s), hi(s));
                     }
-                    tc::tmem_st16(tS + q * 16, pk);
+                    tc::tmem_st16(tP + q * 16, pk);
                 }
                 tc::tmem_st_wait();
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.ds_full));
+                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.ds_full[b]));
             }
             w = x;
             more = more_x;

@@ -144,15 +144,13 @@ __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a_tmem, uint3
                          accumulate);
 }
 
-// The same over 64 rows of X.
+// The same with P in two runs of 32 columns, 64 columns apart (each warpgroup's
+// half over the first columns of its scores).
 template <int D>
-__device__ __forceinline__ void mma_rows64(uint32_t d_tmem, uint32_t a_tmem, uint32_t sX,
-                                           uint32_t accumulate) {
-    constexpr uint32_t kIdesc = tc::idesc_bf16(BM, D, true);
-    const uint64_t desc = tc::sw128_desc(sX, 16384, 1024);
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-        tc::mma_bf16_ts(d_tmem, a_tmem + ks * 8, desc + ks * 128, kIdesc, ks > 0 ? 1u : accumulate);
+__device__ __forceinline__ void mma_rows_2x64(uint32_t d_tmem, uint32_t a_tmem, uint32_t sX,
+                                              uint32_t accumulate) {
+    tc::mma_bf16_ts_2k64(d_tmem, a_tmem, tc::sw128_desc(sX, 16384, 1024), tc::idesc_bf16(BM, D, true),
+                         accumulate);
 }
 
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
