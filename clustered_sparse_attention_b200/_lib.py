@@ -8,6 +8,7 @@ is no CPU path: without the built library every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -157,6 +158,12 @@ def _ptr(t):
 
 def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+def _raw_stream(device):
+    """The current stream's handle; the public accessor builds a Stream object
+    first (3.4 us against 0.3)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _dtype_code(t):
@@ -604,19 +611,20 @@ class Checkpoint:
 def _view(t, name, like=None, shape=None):
     """A token tensor with strides as a Tokens struct.  like: a tensor whose
     device and dtype it must have; shape: its required shape."""
-    if not (t.is_cuda and t.dim() == 4 and t.stride(-1) == 1):
+    st = t.stride()
+    if not (t.is_cuda and len(st) == 4 and st[3] == 1):
         raise ValueError("%s must be a CUDA tensor [B, H, N, d] with d contiguous" % name)
-    _dtype_code(t)
-    if like is not None and (t.device != like.device or t.dtype != like.dtype):
+    if like is None:
+        _dtype_code(t)
+    elif t.dtype != like.dtype or t.device != like.device:
         raise ValueError("%s must be a %s tensor on %s" % (name, like.dtype, like.device))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have the shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
-    return Tokens(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+    return Tokens(t.data_ptr(), st[0], st[1], st[2])
 
 
 def _dense(t, name, dtype, device, shape):
-    if not (t.device == device and t.is_contiguous() and t.dtype == dtype
-            and tuple(t.shape) == tuple(shape)):
+    if not (t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.device == device):
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
                          % (name, dtype, tuple(shape), device))
     return t
@@ -628,21 +636,39 @@ def _new_like(t):
     return out if out.stride(-1) == 1 else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-def _cross_dims(q_shape, K, V, k_len):
+def _on_device(fn):
+    """Runs a call with the device of its first argument as the current one."""
+    @functools.wraps(fn)
+    def call(first, *args, **kw):
+        t = first.codes if isinstance(first, Checkpoint) else first
+        if not t.is_cuda or t.device.index == torch.cuda.current_device():
+            return fn(first, *args, **kw)
+        with torch.cuda.device(t.device):
+            return fn(first, *args, **kw)
+    return call
+
+
+def _cross_dims(q_shape, K, k_len):
     B, Hq, Nq, d = q_shape
-    Bk, Hkv, Nk, dk = K.shape
-    if Bk != B or dk != d:
-        raise ValueError("K must have the shape [%d, Hkv, Nk, %d], not %s" % (B, d, tuple(K.shape)))
+    ks = K.shape
+    if ks[0] != B or ks[3] != d:
+        raise ValueError("K must have the shape [%d, Hkv, Nk, %d], not %s" % (B, d, tuple(ks)))
     if k_len is not None:
         _dense(k_len, "k_len", torch.int32, K.device, (B,))
-    return CrossDims(B, Hq, Hkv, Nq, Nk, d, _dtype_code(K))
+    return CrossDims(B, Hq, ks[1], Nq, ks[2], d, _dtype_code(K))
 
 
-def _cross_workspace(op, dims, device):
-    n = max(int(lib().svgear_cross_workspace_bytes(op, dims)), 256)
+@functools.lru_cache(maxsize=4096)
+def _cross_bytes(op, *dims):
+    return max(int(lib().svgear_cross_workspace_bytes(op, CrossDims(*dims))), 256)
+
+
+def _cross_workspace(op, d, device):
+    n = _cross_bytes(op, d.B, d.Hq, d.Hkv, d.Nq, d.Nk, d.d, d.dtype)
     return torch.empty(n, dtype=torch.uint8, device=device), n
 
 
+@_on_device
 def svgear_cross_attend(Q, K, V, scale=None, k_len=None, O=None, lse=None, check_status=False):
     """Attention of Q [B, Hq, Nq, d] over an encoder's states K, V
     [B, Hkv, Nk, d], Hkv dividing Hq, over the first k_len[b] keys (int32 [B];
@@ -650,100 +676,100 @@ def svgear_cross_attend(Q, K, V, scale=None, k_len=None, O=None, lse=None, check
     strided with d contiguous.  Returns (O, lse): O of Q's type and layout,
     lse float32 [B, Hq, Nq] for the backward pass.  scale defaults to
     1 / sqrt(d)."""
-    q = _view(Q, "Q")
-    with torch.cuda.device(Q.device):
-        k, v = _view(K, "K", Q), _view(V, "V", Q, K.shape)
-        dims = _cross_dims(Q.shape, K, V, k_len)
-        O = _new_like(Q) if O is None else O
-        o = _view(O, "O", Q, Q.shape)
-        if lse is None:
-            lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device)
+    q, k, v = _view(Q, "Q"), _view(K, "K", Q), _view(V, "V", Q, K.shape)
+    dims = _cross_dims(Q.shape, K, k_len)
+    if O is None:
+        O = _new_like(Q)
+    o = _view(O, "O", Q, Q.shape)
+    if lse is None:
+        lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device)
+    else:
         _dense(lse, "lse", torch.float32, Q.device, Q.shape[:3])
-        ws, n = _cross_workspace(CROSS_FORWARD, dims, Q.device)
-        _check("svgear_cross_attend", lib().svgear_cross_attend(
-            q, k, v, dims, _ptr(k_len), float(Q.shape[-1] ** -0.5 if scale is None else scale), o,
-            _ptr(lse), _ptr(ws), n, _stream()))
-        if check_status:
-            _device_status("svgear_cross_attend", ws, n)
+    ws, n = _cross_workspace(CROSS_FORWARD, dims, Q.device)
+    _check("svgear_cross_attend", lib().svgear_cross_attend(
+        q, k, v, dims, _ptr(k_len), float(dims.d ** -0.5 if scale is None else scale), o,
+        lse.data_ptr(), ws.data_ptr(), n, _raw_stream(Q.device)))
+    if check_status:
+        _device_status("svgear_cross_attend", ws, n)
     return O, lse
 
 
+@_on_device
 def svgear_cross_attend_backward(dO, Q, K, V, O, lse, scale=None, k_len=None, check_status=False):
     """Gradients (dQ, dK, dV) of svgear_cross_attend's O, given its O and lse
     and the gradient dO; each of its input's type and layout."""
-    q = _view(Q, "Q")
-    with torch.cuda.device(Q.device):
-        g, o = _view(dO, "dO", Q, Q.shape), _view(O, "O", Q, Q.shape)
-        k, v = _view(K, "K", Q), _view(V, "V", Q, K.shape)
-        dims = _cross_dims(Q.shape, K, V, k_len)
-        _dense(lse, "lse", torch.float32, Q.device, Q.shape[:3])
-        dQ, dK, dV = _new_like(Q), _new_like(K), _new_like(V)
-        ws, n = _cross_workspace(CROSS_BACKWARD, dims, Q.device)
-        _check("svgear_cross_attend_backward", lib().svgear_cross_attend_backward(
-            g, q, k, v, o, _ptr(lse), dims, _ptr(k_len),
-            float(Q.shape[-1] ** -0.5 if scale is None else scale), _view(dQ, "dQ"),
-            _view(dK, "dK"), _view(dV, "dV"), _ptr(ws), n, _stream()))
-        if check_status:
-            _device_status("svgear_cross_attend_backward", ws, n)
+    q, g, o = _view(Q, "Q"), _view(dO, "dO", Q, Q.shape), _view(O, "O", Q, Q.shape)
+    k, v = _view(K, "K", Q), _view(V, "V", Q, K.shape)
+    dims = _cross_dims(Q.shape, K, k_len)
+    _dense(lse, "lse", torch.float32, Q.device, Q.shape[:3])
+    dQ, dK, dV = _new_like(Q), _new_like(K), _new_like(V)
+    ws, n = _cross_workspace(CROSS_BACKWARD, dims, Q.device)
+    _check("svgear_cross_attend_backward", lib().svgear_cross_attend_backward(
+        g, q, k, v, o, lse.data_ptr(), dims, _ptr(k_len),
+        float(dims.d ** -0.5 if scale is None else scale), _view(dQ, "dQ"), _view(dK, "dK"),
+        _view(dV, "dV"), ws.data_ptr(), n, _raw_stream(Q.device)))
+    if check_status:
+        _device_status("svgear_cross_attend_backward", ws, n)
     return dQ, dK, dV
 
 
+@_on_device
 def svgear_checkpoint_save(X):
     """X [B, H, N, d] (strided, d contiguous) in 8 bits: a Checkpoint."""
     x = _view(X, "X")
     B, H, N, d = X.shape
-    with torch.cuda.device(X.device):
-        codes = torch.empty(X.shape, dtype=torch.int8, device=X.device)
-        exps = torch.empty((B, H, N, d // CHECKPOINT_GROUP), dtype=torch.uint8, device=X.device)
-        _check("svgear_checkpoint_save", lib().svgear_checkpoint_save(
-            x, Dims(B, H, N, d, _dtype_code(X)), _ptr(codes), _ptr(exps), _stream()))
+    codes = torch.empty(X.shape, dtype=torch.int8, device=X.device)
+    exps = torch.empty((B, H, N, d // CHECKPOINT_GROUP), dtype=torch.uint8, device=X.device)
+    _check("svgear_checkpoint_save", lib().svgear_checkpoint_save(
+        x, Dims(B, H, N, d, _dtype_code(X)), codes.data_ptr(), exps.data_ptr(),
+        _raw_stream(X.device)))
     return Checkpoint(codes, exps, X.dtype)
 
 
 def _held(c, name, shape=None, device=None, dtype=None):
-    shape = c.codes.shape if shape is None else shape
-    device = c.codes.device if device is None else device
     if not c.codes.is_cuda or c.codes.dim() != 4 or (dtype is not None and c.dtype != dtype):
         raise ValueError("%s must be a Checkpoint of a CUDA %s tensor [B, H, N, d]"
                          % (name, "token" if dtype is None else dtype))
+    shape = c.codes.shape if shape is None else shape
+    device = c.codes.device if device is None else device
     _dense(c.codes, name + ".codes", torch.int8, device, shape)
     _dense(c.exps, name + ".exps", torch.uint8, device,
-           tuple(shape[:3]) + (shape[3] // CHECKPOINT_GROUP,))
-    return _ptr(c.codes), _ptr(c.exps)
+           (shape[0], shape[1], shape[2], shape[3] // CHECKPOINT_GROUP))
+    return c.codes.data_ptr(), c.exps.data_ptr()
 
 
+@_on_device
 def svgear_checkpoint_load(c, out=None):
     """The tensor a Checkpoint stands for, in its type; dense unless `out`."""
     codes, exps = _held(c, "c")
     dev = c.codes.device
-    with torch.cuda.device(dev):
-        if out is None:
-            out = torch.empty(c.codes.shape, dtype=c.dtype, device=dev)
-        x = _view(out, "out", shape=c.codes.shape)
-        if out.device != dev or out.dtype != c.dtype:
-            raise ValueError("out must be a %s tensor on %s" % (c.dtype, dev))
-        B, H, N, d = out.shape
-        _check("svgear_checkpoint_load", lib().svgear_checkpoint_load(
-            codes, exps, Dims(B, H, N, d, _dtype_code(out)), x, _stream()))
+    if out is None:
+        out = torch.empty(c.codes.shape, dtype=c.dtype, device=dev)
+    x = _view(out, "out", shape=c.codes.shape)
+    if out.dtype != c.dtype or out.device != dev:
+        raise ValueError("out must be a %s tensor on %s" % (c.dtype, dev))
+    B, H, N, d = out.shape
+    _check("svgear_checkpoint_load", lib().svgear_checkpoint_load(
+        codes, exps, Dims(B, H, N, d, _dtype_code(out)), x, _raw_stream(dev)))
     return out
 
 
+@_on_device
 def svgear_cross_attend_backward_ckpt(dO, Qc, K, V, Oc, lse, scale=None, k_len=None,
                                       check_status=False):
     """svgear_cross_attend_backward with Q and O read from Checkpoints."""
     g = _view(dO, "dO")
-    with torch.cuda.device(dO.device):
-        qc, qe = _held(Qc, "Qc", dO.shape, dO.device, dO.dtype)
-        oc, oe = _held(Oc, "Oc", dO.shape, dO.device, dO.dtype)
-        k, v = _view(K, "K", dO), _view(V, "V", dO, K.shape)
-        dims = _cross_dims(dO.shape, K, V, k_len)
-        _dense(lse, "lse", torch.float32, dO.device, dO.shape[:3])
-        dQ, dK, dV = _new_like(dO), _new_like(K), _new_like(V)
-        ws, n = _cross_workspace(CROSS_BACKWARD_CKPT, dims, dO.device)
-        _check("svgear_cross_attend_backward_ckpt", lib().svgear_cross_attend_backward_ckpt(
-            g, qc, qe, k, v, oc, oe, _ptr(lse), dims, _ptr(k_len),
-            float(dO.shape[-1] ** -0.5 if scale is None else scale), _view(dQ, "dQ"),
-            _view(dK, "dK"), _view(dV, "dV"), _ptr(ws), n, _stream()))
-        if check_status:
-            _device_status("svgear_cross_attend_backward_ckpt", ws, n)
+    qc, qe = _held(Qc, "Qc", dO.shape, dO.device, dO.dtype)
+    oc, oe = _held(Oc, "Oc", dO.shape, dO.device, dO.dtype)
+    k, v = _view(K, "K", dO), _view(V, "V", dO, K.shape)
+    dims = _cross_dims(dO.shape, K, k_len)
+    _dense(lse, "lse", torch.float32, dO.device, dO.shape[:3])
+    dQ, dK, dV = _new_like(dO), _new_like(K), _new_like(V)
+    ws, n = _cross_workspace(CROSS_BACKWARD_CKPT, dims, dO.device)
+    _check("svgear_cross_attend_backward_ckpt", lib().svgear_cross_attend_backward_ckpt(
+        g, qc, qe, k, v, oc, oe, lse.data_ptr(), dims, _ptr(k_len),
+        float(dims.d ** -0.5 if scale is None else scale), _view(dQ, "dQ"), _view(dK, "dK"),
+        _view(dV, "dV"), ws.data_ptr(), n, _raw_stream(dO.device)))
+    if check_status:
+        _device_status("svgear_cross_attend_backward_ckpt", ws, n)
     return dQ, dK, dV

@@ -793,8 +793,8 @@ int launch_dq(const CrossArgs& a, int* err, int* lost, cudaStream_t st) {
     const void* fn = (const void*)cross_dq_sm100_kernel<D>;
     QMaps m;
     if (!make_tile_map(&m.q, a.Q, a.B, a.Hq, a.Nq, D, BM) || !make_tile_map(&m.g, a.dO, a.B, a.Hq, a.Nq, D, BM) ||
-        !make_row_maps(&m.k, a.K, a.B, a.Hkv, a.Nk, D) ||
-        !make_row_maps(&m.v, a.V, a.B, a.Hkv, a.Nk, D))
+        !make_row_maps(&m.k, a.K, a.B, a.Hkv, a.Nk, D, a.k_len != nullptr) ||
+        !make_row_maps(&m.v, a.V, a.B, a.Hkv, a.Nk, D, a.k_len != nullptr))
         return SVGEAR_ERR_CUDA;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)q_smem<D>()) != cudaSuccess)
         return SVGEAR_ERR_CUDA;

@@ -7,11 +7,14 @@
 // ds_ij = p_ij (do_i.v_j - delta_i), dq_i = scale sum_j ds_ij k_j,
 // dk_j = scale sum_i ds_ij q_i, dv_j = sum_i p_ij do_i.
 //
-// 64 x 64 score tiles, 256 threads in a 16 x 16 grid, 4 x 4 scores and
+// 64 x 64 score tiles, groups of 256 threads in a 16 x 16 grid, 4 x 4 scores and
 // 4 x D/16 outputs a thread: eight (S) or five (P V) shared-memory wavefronts
 // per 32 FMA instructions of a warp, so the FMA pipe is the bound.  Rows of
 // the shared tiles are D + 4 floats (16-byte units an odd number apart), so
-// the 16 column threads read 16 rows without a bank conflict.
+// the 16 column threads read 16 rows without a bank conflict.  The backward
+// kernels' four tiles leave room for one CTA per SM; two groups share it, one
+// for the scores and one for do.v (then dV and dK, or the halves of dQ's
+// columns), which hides twice the latency of one group.
 #include <math.h>
 
 #include "common.cuh"
@@ -23,13 +26,14 @@ namespace {
 
 constexpr int M = kCrossSimtM, N = kCrossSimtN;
 constexpr int kThreads = 256;
+constexpr int kGradThreads = 512;   // two groups
 
 // rows [n0, n0 + 64) of head (b, h) as fp32 rows of D + 4, zeros from n_end on
 template <typename T, int D>
 __device__ __forceinline__ void load_tile(float* s, const svgear_tokens& t, int b, int h, int n0,
                                           int n_end) {
     constexpr int C = Elem<T>::kPerChunk, CH = D / C;
-    for (int i = threadIdx.x; i < 64 * CH; i += kThreads) {
+    for (int i = threadIdx.x; i < 64 * CH; i += blockDim.x) {
         const int r = i / CH, c = (i - r * CH) * C;
         float v[C];
         if (n0 + r < n_end) {
@@ -44,25 +48,25 @@ __device__ __forceinline__ void load_tile(float* s, const svgear_tokens& t, int 
     }
 }
 
-// acc[i][j] = A[4 ty + i] . B[tx + 16 j]
-template <int D>
-__device__ __forceinline__ void dot_tile(const float* A, const float* Bm, int ty, int tx,
-                                         float (&acc)[4][4]) {
+// acc[i][j] = A[4 ty + i] . B[tx + 16 j], j < J (the others 0)
+template <int D, int J>
+__device__ __forceinline__ void dot_columns(const float* A, const float* Bm, int ty, int tx,
+                                            float (&acc)[4][4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
 #pragma unroll 4
     for (int k = 0; k < D; k += 4) {
-        float4 a[4], c[4];
+        float4 a[4], c[J];
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * (D + 4) + k);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[j] = *reinterpret_cast<const float4*>(Bm + (tx + 16 * j) * (D + 4) + k);
+        for (int j = 0; j < J; ++j) c[j] = *reinterpret_cast<const float4*>(Bm + (tx + 16 * j) * (D + 4) + k);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < J; ++j) {
                 acc[i][j] = fmaf(a[i].x, c[j].x, acc[i][j]);
                 acc[i][j] = fmaf(a[i].y, c[j].y, acc[i][j]);
                 acc[i][j] = fmaf(a[i].z, c[j].z, acc[i][j]);
@@ -70,29 +74,48 @@ __device__ __forceinline__ void dot_tile(const float* A, const float* Bm, int ty
             }
     }
 }
-
-// acc[i][4 c + e] += sum_n W[4 ty + i][n] X[n][64 c + 4 tx + e]; W rows of N + 4
+// The same for a tile of `valid` keys: one with at most 16 skips the rest.
 template <int D>
-__device__ __forceinline__ void accumulate(const float* W, const float* X, int ty, int tx,
-                                           float (&acc)[4][D / 16]) {
+__device__ __forceinline__ void dot_tile(const float* A, const float* Bm, int valid, int ty, int tx,
+                                         float (&acc)[4][4]) {
+    if (valid <= 16) dot_columns<D, 1>(A, Bm, ty, tx, acc);
+    else dot_columns<D, 4>(A, Bm, ty, tx, acc);
+}
+
+// acc[i][4 c + e] += sum_n W[4 ty + i][n] X[n][64 c + 4 tx + e]; W rows of N + 4,
+// X rows of D + 4, n < valid (weights past it are 0); C columns (a multiple of
+// 64, or 32: then two per thread)
+template <int D, int C = D>
+__device__ __forceinline__ void accumulate(const float* W, const float* X, int valid, int ty, int tx,
+                                           float (&acc)[4][C / 16]) {
 #pragma unroll 2
-    for (int n = 0; n < N; n += 4) {
+    for (int n = 0; n < min(N, valid); n += 4) {
         float4 w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(W + (4 * ty + i) * (N + 4) + n);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+            const float* row = X + (n + q) * (D + 4);
+            float x[C / 16];
+            if constexpr (C == 32) {
+                const float2 v = *reinterpret_cast<const float2*>(row + 2 * tx);
+                x[0] = v.x;
+                x[1] = v.y;
+            } else {
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                const float4 x = *reinterpret_cast<const float4*>(X + (n + q) * (D + 4) + 64 * c + 4 * tx);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float wi = q == 0 ? w[i].x : q == 1 ? w[i].y : q == 2 ? w[i].z : w[i].w;
-                    acc[i][4 * c] = fmaf(wi, x.x, acc[i][4 * c]);
-                    acc[i][4 * c + 1] = fmaf(wi, x.y, acc[i][4 * c + 1]);
-                    acc[i][4 * c + 2] = fmaf(wi, x.z, acc[i][4 * c + 2]);
-                    acc[i][4 * c + 3] = fmaf(wi, x.w, acc[i][4 * c + 3]);
+                for (int c = 0; c < C / 64; ++c) {
+                    const float4 v = *reinterpret_cast<const float4*>(row + 64 * c + 4 * tx);
+                    x[4 * c] = v.x;
+                    x[4 * c + 1] = v.y;
+                    x[4 * c + 2] = v.z;
+                    x[4 * c + 3] = v.w;
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float wi = q == 0 ? w[i].x : q == 1 ? w[i].y : q == 2 ? w[i].z : w[i].w;
+#pragma unroll
+                for (int c = 0; c < C / 16; ++c) acc[i][c] = fmaf(wi, x[c], acc[i][c]);
             }
         }
     }
@@ -170,7 +193,7 @@ cross_fwd_kernel(CrossArgs a, int splits, int tiles_per_split, float* __restrict
         load_tile<T, D>(sV, a.V, b, hk, t * N, keys);
         __syncthreads();
         float s[4][4];
-        dot_tile<D>(sQ, sK, ty, tx, s);
+        dot_tile<D>(sQ, sK, keys - t * N, ty, tx, s);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float mx = -INFINITY;
@@ -194,7 +217,7 @@ cross_fwd_kernel(CrossArgs a, int splits, int tiles_per_split, float* __restrict
             }
         }
         __syncthreads();
-        accumulate<D>(sP, sV, ty, tx, o);
+        accumulate<D>(sP, sV, keys - t * N, ty, tx, o);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -267,22 +290,31 @@ cross_join_kernel(CrossArgs a, int splits, const float* __restrict__ o_part,
 // ---------------------------------------------------------------------------
 // Backward
 // ---------------------------------------------------------------------------
-// p and ds of one 64 x 64 tile from its scores s and dp
-__device__ __forceinline__ void grad_tile(float (&s)[4][4], float (&dp)[4][4], const float* lse,
-                                          const float* delta, int ty, int tx, int k0, int keys,
-                                          float scale) {
+// p of one 64 x 64 tile from its scores, into W
+__device__ __forceinline__ void put_weights(const float (&s)[4][4], const float* lse, float* W, int ty, int tx,
+                                            int k0, int keys, float scale) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            W[(4 * ty + i) * (N + 4) + tx + 16 * j] =
+                k0 + tx + 16 * j < keys ? expf(s[i][j] * scale - lse[4 * ty + i]) : 0.f;
+}
+// ds = p (dp - delta) of the same tile, p from W, into G (which may be W)
+__device__ __forceinline__ void put_score_grads(const float (&dp)[4][4], const float* delta, const float* W,
+                                                float* G, int ty, int tx) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float p = k0 + tx + 16 * j < keys ? expf(s[i][j] * scale - lse[4 * ty + i]) : 0.f;
-            s[i][j] = p;
-            dp[i][j] = p == 0.f ? 0.f : p * (dp[i][j] - delta[4 * ty + i]);
+            const int x = (4 * ty + i) * (N + 4) + tx + 16 * j;
+            G[x] = W[x] * (dp[i][j] - delta[4 * ty + i]);
         }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) cross_dq_kernel(CrossArgs a) {
+__global__ void __launch_bounds__(kGradThreads) cross_dq_kernel(CrossArgs a) {
+    constexpr int C = D / 2;   // dQ columns of a group
     extern __shared__ float sm[];
     float* sQ = sm;
     float* sG = sQ + M * (D + 4);
@@ -292,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) cross_dq_kernel(CrossArgs a) {
     __shared__ float s_lse[M], s_delta[M];
     const int b = blockIdx.y / a.Hq, h = blockIdx.y - b * a.Hq, hk = h / a.G;
     const int q0 = blockIdx.x * M, keys = cross_keys(a, b);
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const int grp = threadIdx.x >> 8, ty = (threadIdx.x >> 4) & 15, tx = threadIdx.x & 15;
     load_tile<T, D>(sQ, a.Q, b, h, q0, a.Nq);
     load_tile<T, D>(sG, a.dO, b, h, q0, a.Nq);
     if (threadIdx.x < M) {
@@ -301,42 +333,39 @@ __global__ void __launch_bounds__(kThreads) cross_dq_kernel(CrossArgs a) {
         s_lse[threadIdx.x] = row < a.Nq ? a.lse[r] : INFINITY;   // past the end: p = 0
         s_delta[threadIdx.x] = row < a.Nq ? a.delta[r] : 0.f;
     }
-    float dq[4][D / 16];
+    float dq[4][C / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) dq[i][c] = 0.f;
+        for (int c = 0; c < C / 16; ++c) dq[i][c] = 0.f;
     for (int t = 0; t * N < keys; ++t) {
         __syncthreads();
         load_tile<T, D>(sK, a.K, b, hk, t * N, keys);
         load_tile<T, D>(sV, a.V, b, hk, t * N, keys);
         __syncthreads();
-        float s[4][4], dp[4][4];
-        dot_tile<D>(sQ, sK, ty, tx, s);
-        dot_tile<D>(sG, sV, ty, tx, dp);
-        grad_tile(s, dp, s_lse, s_delta, ty, tx, t * N, keys, a.scale);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sS[(4 * ty + i) * (N + 4) + tx + 16 * j] = dp[i][j];
+        float s[4][4];
+        dot_tile<D>(grp ? sG : sQ, grp ? sV : sK, keys - t * N, ty, tx, s);
+        if (grp == 0) put_weights(s, s_lse, sS, ty, tx, t * N, keys, a.scale);
         __syncthreads();
-        accumulate<D>(sS, sK, ty, tx, dq);
+        if (grp == 1) put_score_grads(s, s_delta, sS, sS, ty, tx);
+        __syncthreads();
+        accumulate<D, C>(sS, sK + grp * C, keys - t * N, ty, tx, dq);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int row = q0 + 4 * ty + i;
         if (row >= a.Nq) continue;
-        T* dst = row_ptr<T>(a.dQ, b, h, row);
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-            store4(dst + 64 * c + 4 * tx,
-                   make_float4(dq[i][4 * c] * a.scale, dq[i][4 * c + 1] * a.scale,
-                               dq[i][4 * c + 2] * a.scale, dq[i][4 * c + 3] * a.scale));
+        T* dst = row_ptr<T>(a.dQ, b, h, row) + grp * C;
+        if constexpr (C == 64)
+            store4(dst + 4 * tx, make_float4(dq[i][0] * a.scale, dq[i][1] * a.scale, dq[i][2] * a.scale,
+                                             dq[i][3] * a.scale));
+        else
+            *reinterpret_cast<float2*>(dst + 2 * tx) = make_float2(dq[i][0] * a.scale, dq[i][1] * a.scale);
     }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) cross_dkv_kernel(CrossArgs a, float* __restrict__ part) {
+__global__ void __launch_bounds__(kGradThreads) cross_dkv_kernel(CrossArgs a, float* __restrict__ part) {
     extern __shared__ float sm[];
     float* sQ = sm;
     float* sG = sQ + M * (D + 4);
@@ -345,7 +374,7 @@ __global__ void __launch_bounds__(kThreads) cross_dkv_kernel(CrossArgs a, float*
     float* sP = sV + N * (D + 4);
     float* sS = sP + M * (N + 4);
     __shared__ float s_lse[M], s_delta[M];
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const int grp = threadIdx.x >> 8, ty = (threadIdx.x >> 4) & 15, tx = threadIdx.x & 15;
     const int qtiles = (a.Nq + M - 1) / M;
     const int64_t per = (int64_t)a.G * qtiles;
     const int64_t total = kv_total_units<N>(a) * per;
@@ -359,11 +388,11 @@ __global__ void __launch_bounds__(kThreads) cross_dkv_kernel(CrossArgs a, float*
         __syncthreads();
         load_tile<T, D>(sK, a.K, k.b, k.h, k.kt * N, k.keys);
         load_tile<T, D>(sV, a.V, k.b, k.h, k.kt * N, k.keys);
-        float dk[4][D / 16], dv[4][D / 16];
+        float acc[4][D / 16];   // group 0: dV, group 1: dK
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) dk[i][c] = dv[i][c] = 0.f;
+            for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
         for (int64_t x = first; x < last; ++x) {
             const int g = (int)(x / qtiles), q0 = (int)(x - (int64_t)g * qtiles) * M;
             const int h = k.h * a.G + g;
@@ -377,40 +406,33 @@ __global__ void __launch_bounds__(kThreads) cross_dkv_kernel(CrossArgs a, float*
                 s_delta[threadIdx.x] = row < a.Nq ? a.delta[r] : 0.f;
             }
             __syncthreads();
-            float s[4][4], dp[4][4];
-            dot_tile<D>(sQ, sK, ty, tx, s);
-            dot_tile<D>(sG, sV, ty, tx, dp);
-            grad_tile(s, dp, s_lse, s_delta, ty, tx, k.kt * N, k.keys, a.scale);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    sP[(4 * ty + i) * (N + 4) + tx + 16 * j] = s[i][j];
-                    sS[(4 * ty + i) * (N + 4) + tx + 16 * j] = dp[i][j];
-                }
+            float s[4][4];
+            dot_tile<D>(grp ? sG : sQ, grp ? sV : sK, k.keys - k.kt * N, ty, tx, s);
+            if (grp == 0) put_weights(s, s_lse, sP, ty, tx, k.kt * N, k.keys, a.scale);
             __syncthreads();
-            accumulate_t<D>(sP, sG, ty, tx, dv);
-            accumulate_t<D>(sS, sQ, ty, tx, dk);
+            if (grp == 0) {
+                accumulate_t<D>(sP, sG, ty, tx, acc);
+            } else {
+                put_score_grads(s, s_delta, sP, sS, ty, tx);
+                asm volatile("bar.sync 1, 256;" ::: "memory");   // group 1
+                accumulate_t<D>(sS, sQ, ty, tx, acc);
+            }
         }
         const bool whole = first == 0 && last == per;
-        float* pk = part + ((size_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * 2 * N * D;
+        float* pk = part + (((size_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * 2 + (1 - grp)) * N * D;
+        const float f = grp ? a.scale : 1.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = 4 * ty + i, row = k.kt * N + r;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
                 const int col = 64 * c + 4 * tx;
-                const float4 vk = make_float4(dk[i][4 * c] * a.scale, dk[i][4 * c + 1] * a.scale,
-                                              dk[i][4 * c + 2] * a.scale, dk[i][4 * c + 3] * a.scale);
-                const float4 vv = make_float4(dv[i][4 * c], dv[i][4 * c + 1], dv[i][4 * c + 2],
-                                              dv[i][4 * c + 3]);
-                if (!whole) {
-                    store4(pk + r * D + col, vk);
-                    store4(pk + (N + r) * D + col, vv);
-                } else if (row < k.keys) {
-                    store4(row_ptr<T>(a.dK, k.b, k.h, row) + col, vk);
-                    store4(row_ptr<T>(a.dV, k.b, k.h, row) + col, vv);
-                }
+                const float4 v = make_float4(acc[i][4 * c] * f, acc[i][4 * c + 1] * f, acc[i][4 * c + 2] * f,
+                                             acc[i][4 * c + 3] * f);
+                if (!whole)
+                    store4(pk + r * D + col, v);
+                else if (row < k.keys)
+                    store4(row_ptr<T>(grp ? a.dK : a.dV, k.b, k.h, row) + col, v);
             }
         }
         it += last - first;
@@ -418,53 +440,59 @@ __global__ void __launch_bounds__(kThreads) cross_dkv_kernel(CrossArgs a, float*
 }
 
 // Joins the partial sums of units cut between CTAs (in CTA order) and writes
-// zeros for the keys past k_len.  One CTA per (key tile, b * Hkv + h).
+// zeros for the keys past k_len.  One CTA per 16 rows of a key tile of one
+// (b, key/value head): blockIdx.x = 16-row group, blockIdx.y = b * Hkv + h.
+constexpr int kJoinRows = 16;
 template <typename T, int D, int BN>
 __global__ void __launch_bounds__(256)
 cross_dkv_join_kernel(CrossArgs a, int qrows, int ctas, const float* __restrict__ part) {
-    const int kt = blockIdx.x, b = blockIdx.y / a.Hkv, h = blockIdx.y - b * a.Hkv;
+    const int row0 = blockIdx.x * kJoinRows, kt = row0 / BN;
+    const int b = blockIdx.y / a.Hkv, h = blockIdx.y - b * a.Hkv;
     const int keys = cross_keys(a, b), nt = (keys + BN - 1) / BN;
-    const int64_t per = (int64_t)a.G * ((a.Nq + qrows - 1) / qrows);
-    int64_t before = 0;   // units of the batches before b
-    if (!a.k_len) {
-        before = (int64_t)b * a.Hkv * nt;
-    } else {
-        for (int x = threadIdx.x & 31; x < b; x += 32) before += (cross_keys(a, x) + BN - 1) / BN;
+    const int rows = min(kJoinRows, a.Nk - row0);
+    __shared__ int s_first, s_last;
+    __shared__ bool s_empties;   // some CTAs have no iteration
+    if (threadIdx.x < 32 && kt < nt) {
+        const int64_t per = (int64_t)a.G * ((a.Nq + qrows - 1) / qrows);
+        int64_t before = 0;   // units of the batches before b
+        if (!a.k_len) {
+            before = (int64_t)b * a.Hkv * nt;
+        } else {
+            for (int x = threadIdx.x; x < b; x += 32) before += (cross_keys(a, x) + BN - 1) / BN;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-        before *= a.Hkv;
-    }
-    const int64_t total = kv_total_units<BN>(a) * per;
-    int c0 = 0, c1 = -1;
-    if (kt < nt) {
-        const int64_t s = (before + (int64_t)h * nt + kt) * per, e = s + per;
-        // the CTAs whose ranges hold the unit's first and last iteration
-        int lo = 0, hi = ctas;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (kv_range(total, mid, ctas) <= s) lo = mid; else hi = mid;
+            for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+            before *= a.Hkv;
         }
-        c0 = lo;
-        lo = c0;
-        hi = ctas;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (kv_range(total, mid, ctas) < e) lo = mid; else hi = mid;
+        const int64_t total = kv_total_units<BN>(a) * per;
+        if (threadIdx.x == 0) {
+            // the CTAs whose ranges hold the unit's first and last iteration
+            const int64_t s = (before + (int64_t)h * nt + kt) * per, e = s + per - 1;
+            auto holder = [&](int64_t it) {
+                int c = min(ctas - 1, (int)((double)it / (double)total * ctas));
+                while (c > 0 && kv_range(total, c, ctas) > it) --c;
+                while (c + 1 < ctas && kv_range(total, c + 1, ctas) <= it) ++c;
+                return c;
+            };
+            s_first = holder(s);
+            s_last = holder(e);
+            s_empties = total < ctas;
         }
-        c1 = lo;
     }
-    const int rows = min(BN, a.Nk - kt * BN);
-    const bool direct = kt < nt && c0 == c1;   // written by its CTA, but for the rows past k_len
-    for (int i = threadIdx.x; i < 2 * rows * (D / 4); i += blockDim.x) {
+    __syncthreads();
+    const bool direct = kt < nt && s_first == s_last;   // written by its CTA
+    if (direct && row0 + rows <= keys) return;
+    const int64_t total = direct || kt >= nt || !s_empties ? 0 : kv_total_units<BN>(a) * a.G * ((a.Nq + qrows - 1) / qrows);
+    for (int i = threadIdx.x; i < 2 * rows * (D / 4); i += 256) {
         const int which = i / (rows * (D / 4)), rem = i - which * rows * (D / 4);
-        const int r = rem / (D / 4), col = (rem - r * (D / 4)) * 4, row = kt * BN + r;
+        const int r = rem / (D / 4), col = (rem - r * (D / 4)) * 4, row = row0 + r;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (row < keys) {
             if (direct) continue;
-            for (int c = c0; c <= c1; ++c) {
-                if (kv_range(total, c, ctas) == kv_range(total, c + 1, ctas)) continue;
-                const float4 x = *reinterpret_cast<const float4*>(
-                    part + (((size_t)c * 2 + (c == c0 ? 1 : 0)) * 2 + which) * BN * D + (size_t)r * D + col);
+            const float* src = part + (size_t)(row - kt * BN) * D + col + (size_t)which * BN * D;
+            for (int c = s_first; c <= s_last; ++c) {
+                if (s_empties && kv_range(total, c, ctas) == kv_range(total, c + 1, ctas)) continue;
+                const float4 x =
+                    *reinterpret_cast<const float4*>(src + ((size_t)c * 2 + (c == s_first ? 1 : 0)) * 2 * BN * D);
                 v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
             }
         }
@@ -573,7 +601,7 @@ template <typename T, int D>
 int dq(const CrossArgs& a, cudaStream_t st) {
     const size_t smem = sizeof(float) * (4 * 64 * (D + 4) + M * (N + 4));
     if (int s = set_smem(cross_dq_kernel<T, D>, smem)) return s;
-    cross_dq_kernel<T, D><<<dim3(ceil_div(a.Nq, M), a.B * a.Hq), kThreads, smem, st>>>(a);
+    cross_dq_kernel<T, D><<<dim3(ceil_div(a.Nq, M), a.B * a.Hq), kGradThreads, smem, st>>>(a);
     count_launches(1);
     SVGEAR_LAUNCH_CHECK();
     return SVGEAR_OK;
@@ -582,7 +610,7 @@ template <typename T, int D>
 int dkv(const CrossArgs& a, int ctas, float* part, cudaStream_t st) {
     const size_t smem = sizeof(float) * (4 * 64 * (D + 4) + 2 * M * (N + 4));
     if (int s = set_smem(cross_dkv_kernel<T, D>, smem)) return s;
-    cross_dkv_kernel<T, D><<<ctas, kThreads, smem, st>>>(a, part);
+    cross_dkv_kernel<T, D><<<ctas, kGradThreads, smem, st>>>(a, part);
     count_launches(1);
     SVGEAR_LAUNCH_CHECK();
     return SVGEAR_OK;
@@ -590,7 +618,7 @@ int dkv(const CrossArgs& a, int ctas, float* part, cudaStream_t st) {
 template <typename T, int D>
 int dkv_join(const CrossArgs& a, int rows, int ctas, const float* part, cudaStream_t st) {
     constexpr int BN = sizeof(T) == 4 ? kCrossSimtN : kCrossTcN;
-    cross_dkv_join_kernel<T, D, BN><<<dim3(ceil_div(a.Nk, BN), a.B * a.Hkv), 256, 0, st>>>(a, rows, ctas, part);
+    cross_dkv_join_kernel<T, D, BN><<<dim3(ceil_div(a.Nk, kJoinRows), a.B * a.Hkv), 256, 0, st>>>(a, rows, ctas, part);
     count_launches(1);
     SVGEAR_LAUNCH_CHECK();
     return SVGEAR_OK;

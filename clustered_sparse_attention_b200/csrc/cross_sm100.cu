@@ -513,8 +513,8 @@ int launch(const CrossArgs& a, const Plan& plan, float* o_part, float* lse_part,
     if (launch_regs < kMinLaunchRegs) return SVGEAR_ERR_UNSUPPORTED;
     Maps maps;
     if (!make_tile_map(&maps.q, a.Q, a.B, a.Hq, a.Nq, D) || !make_tile_map(&maps.o, a.O, a.B, a.Hq, a.Nq, D, 32) ||
-        !make_row_maps(&maps.k, a.K, a.B, a.Hkv, a.Nk, D) ||
-        !make_row_maps(&maps.v, a.V, a.B, a.Hkv, a.Nk, D))
+        !make_row_maps(&maps.k, a.K, a.B, a.Hkv, a.Nk, D, a.k_len != nullptr) ||
+        !make_row_maps(&maps.v, a.V, a.B, a.Hkv, a.Nk, D, a.k_len != nullptr))
         return SVGEAR_ERR_CUDA;
     const size_t smem = (size_t)(2 + ring_slots<D>()) * (D / 64) * 16384 + 8 * 4096 + 1024;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)

@@ -26,10 +26,11 @@ struct TileMap {
     int hmul, bmul;
 };
 
-inline bool make_row_maps(RowMaps* m, const svgear_tokens& t, int B, int H, int N, int D) {
+// pieces: the smaller boxes too, for batches with key counts of their own.
+inline bool make_row_maps(RowMaps* m, const svgear_tokens& t, int B, int H, int N, int D, bool pieces) {
     m->hmul = t.stride_h != 0;
     m->bmul = t.stride_b != 0;
-    for (int i = 0; i < 8; ++i)
+    for (int i = pieces ? 0 : 7; i < 8; ++i)
         if (!make_tokens_map(&m->box[i], t, B, H, N, D, 1u << i)) return false;
     return true;
 }
