@@ -20,6 +20,7 @@
 #include "common.cuh"
 #include "cross.h"
 #include "launchers.h"
+#include "tc_ptx.cuh"
 
 namespace svgear {
 namespace {
@@ -28,23 +29,16 @@ constexpr int M = kCrossSimtM, N = kCrossSimtN;
 constexpr int kThreads = 256;
 constexpr int kGradThreads = 512;   // two groups
 
-// rows [n0, n0 + 64) of head (b, h) as fp32 rows of D + 4, zeros from n_end on
-template <typename T, int D>
-__device__ __forceinline__ void load_tile(float* s, const svgear_tokens& t, int b, int h, int n0,
-                                          int n_end) {
-    constexpr int C = Elem<T>::kPerChunk, CH = D / C;
+// Starts the copy of rows [n0, n0 + 64) of head (b, h) to fp32 rows of D + 4,
+// zeros from n_end on (part of the thread's next cp.async group).
+template <int D>
+__device__ __forceinline__ void copy_tile(float* s, const svgear_tokens& t, int b, int h, int n0, int n_end) {
+    constexpr int CH = D / 4;
     for (int i = threadIdx.x; i < 64 * CH; i += blockDim.x) {
-        const int r = i / CH, c = (i - r * CH) * C;
-        float v[C];
-        if (n0 + r < n_end) {
-            Elem<T>::load(row_ptr<const T>(t, b, h, n0 + r) + c, v);
-        } else {
-#pragma unroll
-            for (int e = 0; e < C; ++e) v[e] = 0.f;
-        }
-        float4* d4 = reinterpret_cast<float4*>(s + r * (D + 4) + c);
-#pragma unroll
-        for (int e = 0; e < C; e += 4) d4[e / 4] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        const int r = i / CH, c = (i - r * CH) * 4;
+        const bool in = n0 + r < n_end;
+        const float* src = row_ptr<const float>(t, b, h, in ? n0 + r : 0) + c;
+        tc::cp_async16(tc::smem_u32(s + r * (D + 4) + c), src, in ? 16u : 0u);
     }
 }
 
@@ -163,7 +157,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
     *reinterpret_cast<uint2*>(p) = u;
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
 cross_fwd_kernel(CrossArgs a, int splits, int tiles_per_split, float* __restrict__ o_part,
                  float* __restrict__ lse_part) {
@@ -178,7 +172,7 @@ cross_fwd_kernel(CrossArgs a, int splits, int tiles_per_split, float* __restrict
     const int t0 = sp * tiles_per_split, t1 = min((keys + N - 1) / N, t0 + tiles_per_split);
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
 
-    load_tile<T, D>(sQ, a.Q, b, h, q0, a.Nq);
+    copy_tile<D>(sQ, a.Q, b, h, q0, a.Nq);
     float m[4], l[4], o[4][D / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -189,8 +183,11 @@ cross_fwd_kernel(CrossArgs a, int splits, int tiles_per_split, float* __restrict
     }
     for (int t = t0; t < t1; ++t) {
         __syncthreads();
-        load_tile<T, D>(sK, a.K, b, hk, t * N, keys);
-        load_tile<T, D>(sV, a.V, b, hk, t * N, keys);
+        copy_tile<D>(sK, a.K, b, hk, t * N, keys);
+        tc::cp_async_commit();
+        copy_tile<D>(sV, a.V, b, hk, t * N, keys);   // arrives beside the scores
+        tc::cp_async_commit();
+        tc::cp_async_wait<1>();
         __syncthreads();
         float s[4][4];
         dot_tile<D>(sQ, sK, keys - t * N, ty, tx, s);
@@ -216,6 +213,7 @@ cross_fwd_kernel(CrossArgs a, int splits, int tiles_per_split, float* __restrict
                 sP[(4 * ty + i) * (N + 4) + tx + 16 * j] = p;
             }
         }
+        tc::cp_async_wait<0>();
         __syncthreads();
         accumulate<D>(sP, sV, keys - t * N, ty, tx, o);
     }
@@ -237,7 +235,7 @@ cross_fwd_kernel(CrossArgs a, int splits, int tiles_per_split, float* __restrict
                                    o[i][4 * c + 3] * inv));
         } else {
             if (tx == 0) a.lse[r] = lse;
-            T* dst = row_ptr<T>(a.O, b, h, row);
+            float* dst = row_ptr<float>(a.O, b, h, row);
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
                 store4(dst + 64 * c + 4 * tx,
@@ -312,21 +310,23 @@ __device__ __forceinline__ void put_score_grads(const float (&dp)[4][4], const f
         }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kGradThreads) cross_dq_kernel(CrossArgs a) {
     constexpr int C = D / 2;   // dQ columns of a group
     extern __shared__ float sm[];
     float* sQ = sm;
     float* sG = sQ + M * (D + 4);
-    float* sK = sG + M * (D + 4);
-    float* sV = sK + N * (D + 4);
-    float* sS = sV + N * (D + 4);
+    float* sKV = sG + M * (D + 4);                 // K and V of two tiles
+    float* sS = sKV + 4 * N * (D + 4);
     __shared__ float s_lse[M], s_delta[M];
     const int b = blockIdx.y / a.Hq, h = blockIdx.y - b * a.Hq, hk = h / a.G;
     const int q0 = blockIdx.x * M, keys = cross_keys(a, b);
     const int grp = threadIdx.x >> 8, ty = (threadIdx.x >> 4) & 15, tx = threadIdx.x & 15;
-    load_tile<T, D>(sQ, a.Q, b, h, q0, a.Nq);
-    load_tile<T, D>(sG, a.dO, b, h, q0, a.Nq);
+    copy_tile<D>(sQ, a.Q, b, h, q0, a.Nq);
+    copy_tile<D>(sG, a.dO, b, h, q0, a.Nq);
+    copy_tile<D>(sKV, a.K, b, hk, 0, keys);
+    copy_tile<D>(sKV + N * (D + 4), a.V, b, hk, 0, keys);
+    tc::cp_async_commit();
     if (threadIdx.x < M) {
         const int row = q0 + threadIdx.x;
         const size_t r = (size_t)blockIdx.y * a.Nq + row;
@@ -339,10 +339,16 @@ __global__ void __launch_bounds__(kGradThreads) cross_dq_kernel(CrossArgs a) {
 #pragma unroll
         for (int c = 0; c < C / 16; ++c) dq[i][c] = 0.f;
     for (int t = 0; t * N < keys; ++t) {
+        float* sK = sKV + (t & 1) * 2 * N * (D + 4);
+        float* sV = sK + N * (D + 4);
+        tc::cp_async_wait<0>();
         __syncthreads();
-        load_tile<T, D>(sK, a.K, b, hk, t * N, keys);
-        load_tile<T, D>(sV, a.V, b, hk, t * N, keys);
-        __syncthreads();
+        if ((t + 1) * N < keys) {   // the next tile arrives beside this one's arithmetic
+            float* next = sKV + ((t + 1) & 1) * 2 * N * (D + 4);
+            copy_tile<D>(next, a.K, b, hk, (t + 1) * N, keys);
+            copy_tile<D>(next + N * (D + 4), a.V, b, hk, (t + 1) * N, keys);
+        }
+        tc::cp_async_commit();
         float s[4][4];
         dot_tile<D>(grp ? sG : sQ, grp ? sV : sK, keys - t * N, ty, tx, s);
         if (grp == 0) put_weights(s, s_lse, sS, ty, tx, t * N, keys, a.scale);
@@ -351,11 +357,12 @@ __global__ void __launch_bounds__(kGradThreads) cross_dq_kernel(CrossArgs a) {
         __syncthreads();
         accumulate<D, C>(sS, sK + grp * C, keys - t * N, ty, tx, dq);
     }
+    tc::cp_async_wait<0>();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int row = q0 + 4 * ty + i;
         if (row >= a.Nq) continue;
-        T* dst = row_ptr<T>(a.dQ, b, h, row) + grp * C;
+        float* dst = row_ptr<float>(a.dQ, b, h, row) + grp * C;
         if constexpr (C == 64)
             store4(dst + 4 * tx, make_float4(dq[i][0] * a.scale, dq[i][1] * a.scale, dq[i][2] * a.scale,
                                              dq[i][3] * a.scale));
@@ -364,11 +371,11 @@ __global__ void __launch_bounds__(kGradThreads) cross_dq_kernel(CrossArgs a) {
     }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kGradThreads) cross_dkv_kernel(CrossArgs a, float* __restrict__ part) {
     extern __shared__ float sm[];
-    float* sQ = sm;
-    float* sG = sQ + M * (D + 4);
+    float* sQ2 = sm;                               // Q of two tiles
+    float* sG = sQ2 + 2 * M * (D + 4);
     float* sK = sG + M * (D + 4);
     float* sV = sK + N * (D + 4);
     float* sP = sV + N * (D + 4);
@@ -386,8 +393,15 @@ __global__ void __launch_bounds__(kGradThreads) cross_dkv_kernel(CrossArgs a, fl
         const int64_t first = it - u * per, last = min(per, first + (end - it));
         const KvUnit k = kv_unit<N>(a, cur, u);
         __syncthreads();
-        load_tile<T, D>(sK, a.K, k.b, k.h, k.kt * N, k.keys);
-        load_tile<T, D>(sV, a.V, k.b, k.h, k.kt * N, k.keys);
+        copy_tile<D>(sK, a.K, k.b, k.h, k.kt * N, k.keys);
+        copy_tile<D>(sV, a.V, k.b, k.h, k.kt * N, k.keys);
+        const int valid = k.keys - k.kt * N;
+        auto copy_q = [&](int64_t x) {
+            const int g = (int)(x / qtiles);
+            copy_tile<D>(sQ2 + (x & 1) * M * (D + 4), a.Q, k.b, k.h * a.G + g, (int)(x - (int64_t)g * qtiles) * M, a.Nq);
+        };
+        copy_q(first);
+        tc::cp_async_commit();
         float acc[4][D / 16];   // group 0: dV, group 1: dK
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -396,26 +410,30 @@ __global__ void __launch_bounds__(kGradThreads) cross_dkv_kernel(CrossArgs a, fl
         for (int64_t x = first; x < last; ++x) {
             const int g = (int)(x / qtiles), q0 = (int)(x - (int64_t)g * qtiles) * M;
             const int h = k.h * a.G + g;
+            const float* sQ = sQ2 + (x & 1) * M * (D + 4);
             __syncthreads();
-            load_tile<T, D>(sQ, a.Q, k.b, h, q0, a.Nq);
-            load_tile<T, D>(sG, a.dO, k.b, h, q0, a.Nq);
+            copy_tile<D>(sG, a.dO, k.b, h, q0, a.Nq);
+            tc::cp_async_commit();
+            if (x + 1 < last) copy_q(x + 1);   // arrives beside this tile's arithmetic
+            tc::cp_async_commit();
             if (threadIdx.x < M) {
                 const int row = q0 + threadIdx.x;
                 const size_t r = ((size_t)k.b * a.Hq + h) * a.Nq + row;
                 s_lse[threadIdx.x] = row < a.Nq ? a.lse[r] : INFINITY;
                 s_delta[threadIdx.x] = row < a.Nq ? a.delta[r] : 0.f;
             }
+            tc::cp_async_wait<1>();
             __syncthreads();
             float s[4][4];
-            dot_tile<D>(grp ? sG : sQ, grp ? sV : sK, k.keys - k.kt * N, ty, tx, s);
+            dot_tile<D>(grp ? sG : sQ, grp ? sV : sK, valid, ty, tx, s);
             if (grp == 0) put_weights(s, s_lse, sP, ty, tx, k.kt * N, k.keys, a.scale);
             __syncthreads();
             if (grp == 0) {
-                accumulate_t<D>(sP, sG, ty, tx, acc);
+                if (4 * ty < valid) accumulate_t<D>(sP, sG, ty, tx, acc);   // rows past the keys are not written
             } else {
                 put_score_grads(s, s_delta, sP, sS, ty, tx);
                 asm volatile("bar.sync 1, 256;" ::: "memory");   // group 1
-                accumulate_t<D>(sS, sQ, ty, tx, acc);
+                if (4 * ty < valid) accumulate_t<D>(sS, sQ, ty, tx, acc);
             }
         }
         const bool whole = first == 0 && last == per;
@@ -432,10 +450,11 @@ __global__ void __launch_bounds__(kGradThreads) cross_dkv_kernel(CrossArgs a, fl
                 if (!whole)
                     store4(pk + r * D + col, v);
                 else if (row < k.keys)
-                    store4(row_ptr<T>(grp ? a.dK : a.dV, k.b, k.h, row) + col, v);
+                    store4(row_ptr<float>(grp ? a.dK : a.dV, k.b, k.h, row) + col, v);
             }
         }
         it += last - first;
+        tc::cp_async_wait<0>();
     }
 }
 
@@ -568,11 +587,11 @@ int set_smem(F* fn, size_t bytes) {
                : SVGEAR_ERR_CUDA;
 }
 
-template <typename T, int D>
+template <int D>
 int fwd(const CrossArgs& a, CrossSplit sp, float* o_part, float* lse_part, cudaStream_t st) {
     const size_t smem = sizeof(float) * (3 * 64 * (D + 4) + M * (N + 4));
-    if (int s = set_smem(cross_fwd_kernel<T, D>, smem)) return s;
-    cross_fwd_kernel<T, D><<<dim3((unsigned)ceil_div(a.Nq, M) * sp.splits, a.B * a.Hq), kThreads, smem, st>>>(
+    if (int s = set_smem(cross_fwd_kernel<D>, smem)) return s;
+    cross_fwd_kernel<D><<<dim3((unsigned)ceil_div(a.Nq, M) * sp.splits, a.B * a.Hq), kThreads, smem, st>>>(
         a, sp.splits, sp.tiles, o_part, lse_part);
     count_launches(1);
     SVGEAR_LAUNCH_CHECK();
@@ -597,20 +616,20 @@ int delta(const CrossArgs& a, const HeldTokens* q, const HeldTokens* o, void* qx
     SVGEAR_LAUNCH_CHECK();
     return SVGEAR_OK;
 }
-template <typename T, int D>
+template <int D>
 int dq(const CrossArgs& a, cudaStream_t st) {
-    const size_t smem = sizeof(float) * (4 * 64 * (D + 4) + M * (N + 4));
-    if (int s = set_smem(cross_dq_kernel<T, D>, smem)) return s;
-    cross_dq_kernel<T, D><<<dim3(ceil_div(a.Nq, M), a.B * a.Hq), kGradThreads, smem, st>>>(a);
+    const size_t smem = sizeof(float) * (6 * 64 * (D + 4) + M * (N + 4));
+    if (int s = set_smem(cross_dq_kernel<D>, smem)) return s;
+    cross_dq_kernel<D><<<dim3(ceil_div(a.Nq, M), a.B * a.Hq), kGradThreads, smem, st>>>(a);
     count_launches(1);
     SVGEAR_LAUNCH_CHECK();
     return SVGEAR_OK;
 }
-template <typename T, int D>
+template <int D>
 int dkv(const CrossArgs& a, int ctas, float* part, cudaStream_t st) {
-    const size_t smem = sizeof(float) * (4 * 64 * (D + 4) + 2 * M * (N + 4));
-    if (int s = set_smem(cross_dkv_kernel<T, D>, smem)) return s;
-    cross_dkv_kernel<T, D><<<ctas, kGradThreads, smem, st>>>(a, part);
+    const size_t smem = sizeof(float) * (5 * 64 * (D + 4) + 2 * M * (N + 4));
+    if (int s = set_smem(cross_dkv_kernel<D>, smem)) return s;
+    cross_dkv_kernel<D><<<ctas, kGradThreads, smem, st>>>(a, part);
     count_launches(1);
     SVGEAR_LAUNCH_CHECK();
     return SVGEAR_OK;
@@ -633,8 +652,8 @@ using bf16 = __nv_bfloat16;
 
 int launch_cross_simt(const CrossArgs& a, CrossSplit sp, float* o_part, float* lse_part,
                       cudaStream_t st) {
-    return a.D == 128 ? fwd<float, 128>(a, sp, o_part, lse_part, st)
-                      : fwd<float, 64>(a, sp, o_part, lse_part, st);
+    return a.D == 128 ? fwd<128>(a, sp, o_part, lse_part, st)
+                      : fwd<64>(a, sp, o_part, lse_part, st);
 }
 int launch_cross_join(const CrossArgs& a, int dtype, int splits, const float* o_part,
                       const float* lse_part, cudaStream_t st) {
@@ -649,9 +668,9 @@ int launch_cross_dkv_join(const CrossArgs& a, int dtype, int rows, int ctas, con
     return SVGEAR_PICK(dkv_join, a, rows, ctas, part, st);
 }
 int launch_cross_backward_simt(const CrossArgs& a, int ctas, float* part, cudaStream_t st) {
-    int s = a.D == 128 ? dq<float, 128>(a, st) : dq<float, 64>(a, st);
+    int s = a.D == 128 ? dq<128>(a, st) : dq<64>(a, st);
     if (s) return s;
-    if ((s = a.D == 128 ? dkv<float, 128>(a, ctas, part, st) : dkv<float, 64>(a, ctas, part, st))) return s;
+    if ((s = a.D == 128 ? dkv<128>(a, ctas, part, st) : dkv<64>(a, ctas, part, st))) return s;
     return launch_cross_dkv_join(a, SVGEAR_F32, M, ctas, part, st);
 }
 
