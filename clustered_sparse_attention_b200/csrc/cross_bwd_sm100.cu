@@ -34,20 +34,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int HN = 64;   // columns of a tile per warpgroup
 constexpr uint32_t kTmemCols = 512;
 
-// Rewrites columns >= valid of this warp's HN score columns at taddr to -inf.
-__device__ __forceinline__ void mask_columns(uint32_t taddr, int valid) {
-#pragma unroll 1
-    for (int c4 = max(valid, 0) / 32; c4 < HN / 32; ++c4) {
-        uint32_t t[32];
-        tc::tmem_ld32(taddr + c4 * 32, t);
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-            if (c4 * 32 + e >= valid) t[e] = __float_as_uint(-INFINITY);
-        tc::tmem_st32(taddr + c4 * 32, t);
-    }
-    tc::tmem_st_wait();
-}
 // (a, b) - (c, c) on packed fp32 pairs
 __device__ __forceinline__ uint64_t sub2(uint32_t a, uint32_t b, uint64_t neg) {
     uint64_t r;
@@ -62,21 +48,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ float lo(uint64_t x) { return __uint_as_float((uint32_t)x); }
 __device__ __forceinline__ float hi(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
-
-// One thread's MMAs are complete once `bar` flips; if that wait expires TMEM
-// stays allocated and the device's lost word stops every later tensor-core
-// kernel before it allocates.
-__device__ __forceinline__ void drain_mma(uint64_t* bar, int* keep_tmem, int* err, int* lost, int where) {
-    tc::commit(tc::smem_u32(bar));
-    if (!tc::drain_bar(bar, 0)) {
-        *keep_tmem = 1;
-        tc::mark_tmem_lost(lost);
-        if (atomicCAS(err, 0, SVGEAR_ERR_TIMEOUT) == 0) {
-            err[1] = where;
-            err[2] = blockIdx.x;
-        }
-    }
-}
 
 // ---------------------------------------------------------------------------
 // dK, dV: a persistent CTA per SM takes an equal share of the iterations (key
@@ -688,7 +659,7 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
                 if (!(ok = warp_poll_bar(&sh.s_full, g & 1, abort_flag, err, (11 << 16)))) break;
                 tc::fence_after_sync();
                 const int valid = w.keys - j * BN - h * HN;
-                if (valid < HN) mask_columns(tS, valid);   // past the keys: p = 0
+                if (valid < HN) mask_columns<HN>(tS, valid);   // past the keys: p = 0
                 uint32_t v[HN];
                 tc::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
                 tc::tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
@@ -775,13 +746,7 @@ int launch_dkv(const CrossArgs& a, float* part, int* err, int* lost, cudaStream_
     if (!make_tile_map(&m.q, a.Q, a.B, a.Hq, a.Nq, D, BM) || !make_tile_map(&m.g, a.dO, a.B, a.Hq, a.Nq, D, BM) ||
         !make_tile_map(&m.k, a.K, a.B, a.Hkv, a.Nk, D, BM) || !make_tile_map(&m.v, a.V, a.B, a.Hkv, a.Nk, D, BM))
         return SVGEAR_ERR_CUDA;
-    // the swizzled tiles need 1024-byte alignment: the dynamic part starts after
-    // the static one, which is padded to a multiple of it
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, fn) != cudaSuccess) return SVGEAR_ERR_CUDA;
-    if (fa.sharedSizeBytes % 1024 != 0) return SVGEAR_ERR_UNSUPPORTED;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kv_smem<D>()) != cudaSuccess)
-        return SVGEAR_ERR_CUDA;
+    if (int s = set_aligned_smem(fn, kv_smem<D>())) return s;
     cross_dkv_sm100_kernel<D><<<kSms, kKvThreads, kv_smem<D>(), st>>>(m, a, part, err, lost);
     count_launches(1);
     SVGEAR_LAUNCH_CHECK();

@@ -2,28 +2,23 @@
 // TMEM (sm_100a).
 //
 // o_i = sum_j e^{s_ij - m} v_j / l in one pass over the keys with the running
-// maximum m and sum l; the weights enter the product with V as bf16 (their
-// rounding, 2^-9 of each on average, is of the size of the output's own), l
-// and all statistics stay fp32.
+// maximum m and sum l.  The weights enter the product with V rounded to bf16
+// (an error of the size of the output's own rounding); l and all statistics
+// stay fp32.
 //
-// One persistent CTA per SM.  An item is 256 query rows of one head: two
-// 128-row tiles ("halves") that share every K and V tile, so each shared
-// memory byte feeds two MMAs.  12 warps:
-//   0-3, 4-7  softmax of half 0 / 1, one row per thread (TMEM lane = row);
-//   8         TMA producer: Q tiles, and K and V tiles through one slot ring;
-//   9, 10     one thread each issues the MMAs of half 0 / 1, so a half waits
-//             only for its own softmax: while one half exponentiates, the
-//             other's PV and next QK use the tensor cores;
-//   11        idle.
-// TMEM: S0 | S1 | O0 | O1; P (bf16) overwrites the first 64 columns of its S.
-// The Q tiles of the next item are copied as soon as the last QK has read
-// them, and its K tiles follow through the ring, so items overlap except for
-// a half's own epilogue.
-//
-// With few rows (Nq <= 128) over many keys one half would leave the other
-// idle: both then take the same rows ("solo"), half h the tiles h, h + 2, ...
-// of the item, and their partial results are joined like those of the key
-// splits (cross_join_kernel).
+// One persistent CTA per SM; an item is 128 query rows of one head (and one
+// split of its keys).  16 warps:
+//   0-3, 4-7  softmax warpgroups, one row per thread (TMEM lane = row):
+//             warpgroup h takes keys [64h, 64h + 64) of every 128-key tile
+//             with its own running maximum, sum and accumulator O_h;
+//   8, 11     TMA producers of Q and K tiles and of V tiles (a ring each);
+//   9, 10     issue S = Q K^T and O_h += P_h V;
+//   12-15     epilogue: merges the two accumulators like partial attentions and
+//             writes the rows, while the softmax is in the next item.
+// TMEM: S | P[0] | P[1] | O_0 | O_1 (128 + 64 + 64 + d + d columns).  Over the
+// CTA's tiles g = 0, 1, ... of all its items, S(g + 1) is issued as soon as the
+// softmax has S(g) in registers and P(g) goes to a buffer of its own, so that
+// neither product is on the path from one tile's softmax to the next one's.
 //
 // Every wait is bounded (tc_wait.cuh).
 #include <math.h>
@@ -39,92 +34,88 @@ using bf16 = __nv_bfloat16;
 using tc::poll_bar;
 using tc::warp_poll_bar;
 
-constexpr int kProducerWarp = 8;
-constexpr int kMmaWarp = 9;             // and 10 for half 1
-constexpr int kThreads = 12 * 32;
-// Register split as launched (168 x 384): 232 for the softmax warpgroups, 40
-// for the others.
-constexpr uint32_t kSoftmaxRegs = 232;
-constexpr uint32_t kIssueRegs = 40;
-constexpr int kMinLaunchRegs = 168;
-static_assert(2 * 128 * kSoftmaxRegs + 128 * kIssueRegs <= kMinLaunchRegs * kThreads,
-              "register split exceeds the launch allocation");
+constexpr int kThreads = 16 * 32;
+constexpr int kLoadWarp = 8, kQkWarp = 9, kPvWarp = 10, kVWarp = 11, kEpilogueWarp = 12;
+constexpr int HN = BN / 2;                  // keys of a warpgroup per tile
 constexpr uint32_t kTmemCols = 512;
-constexpr int kTurnChunk = 2;               // 32-column chunk after which the turn passes
+constexpr uint32_t kP = BN, kO = 2 * BN;    // TMEM columns of P[0] and O_0
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
+constexpr int kMinSplitTiles = 2;           // fewest key tiles of a split
 
+// A copy takes some 2,000 cycles to arrive and S(g + 2) follows S(g + 1) by one
+// tile's softmax (1,500): three K slots.  V(g + 2) has two tiles' time.
 template <int D>
-constexpr int ring_slots() { return D == 128 ? 4 : 8; }
+constexpr int k_slots() { return D == 128 ? 3 : 4; }
+template <int D>
+constexpr int v_slots() { return D == 128 ? 2 : 4; }
+template <int D>
+constexpr uint32_t smem_bytes() { return (2 + k_slots<D>() + v_slots<D>()) * (D / 64) * 16384; }
 
 struct Maps {
     RowMaps k, v;
-    TileMap q, o;   // o: boxes of 32 rows
+    TileMap q;
 };
 
 struct Shared {
-    uint64_t q_full[2], q_empty[2];   // the half's Q tile
-    uint64_t full[8], empty[8];       // K/V slots
-    uint64_t s_full[2], p_full[2];    // S written / P written
-    uint64_t o_full[2], o_free[2];    // O final / read out
-    uint64_t turn[2];                 // half h may exponentiate its next paired tile
+    uint64_t q_full[2], q_empty[2];
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t s_full, s_read;
+    uint64_t p_full[2], p_free[2];    // P[b] written / read by both PV
+    uint64_t o_full, o_free;          // O_0 and O_1 final / read out
+    uint64_t ml_full;                 // both warpgroups' (m, l) of the item
     uint64_t drain[2];
+    float2 ml[2][BM];                 // [h][row]
     uint32_t tmem_base;
     int abort_flag;
     int keep_tmem;
 };
 
 struct Plan {
-    int qpairs;       // 256-row pairs per head
+    int qtiles;       // 128-row tiles per head
     int splits;       // key splits
     int tiles;        // key tiles per split
-    int solo;         // both halves on the same 128 rows
     int items;
 };
 
-// The items of one CTA in turn: item = ((b * Hq + h) * splits + split) * qpairs +
-// pair, advanced by the grid digit by digit (divisions once per CTA: they
-// would sit on every role's path between items).
+// The items of one CTA in turn: item = ((b * Hq + h) * splits + split) * qtiles +
+// tile, advanced by the grid digit by digit (divisions once per CTA: they would
+// sit on every role's path between items).
 struct Work {
-    int item, qp, split, h, b;        // digits
+    int item, qt, split, h, b;        // digits
     int dq, ds, dh, db;               // the grid's digits
-    int hk, q0, keys;
+    int hk, keys;
     int t0, T;                        // first key tile and number of tiles
     __device__ __forceinline__ void derive(const CrossArgs& a, const Plan& p) {
-        q0 = qp * 2 * BM;
         keys = cross_keys(a, b);
         t0 = split * p.tiles;
         T = max(0, min((keys + BN - 1) / BN - t0, p.tiles));
         hk = a.G == 1 ? h : h / a.G;
     }
-    __device__ __forceinline__ void start(const CrossArgs& a, const Plan& p) {
+    __device__ __forceinline__ bool start(const CrossArgs& a, const Plan& p) {
         item = blockIdx.x;
         int x = item;
-        qp = x % p.qpairs; x /= p.qpairs;
+        qt = x % p.qtiles; x /= p.qtiles;
         split = x % p.splits; x /= p.splits;
         h = x % a.Hq;
         b = x / a.Hq;
         x = gridDim.x;
-        dq = x % p.qpairs; x /= p.qpairs;
+        dq = x % p.qtiles; x /= p.qtiles;
         ds = x % p.splits; x /= p.splits;
         dh = x % a.Hq;
         db = x / a.Hq;
         if (item < p.items) derive(a, p);
+        return item < p.items;
     }
-    __device__ __forceinline__ void next(const CrossArgs& a, const Plan& p) {
+    __device__ __forceinline__ bool next(const CrossArgs& a, const Plan& p) {
         item += gridDim.x;
-        qp += dq; split += ds; h += dh; b += db;
-        if (qp >= p.qpairs) { qp -= p.qpairs; ++split; }
+        qt += dq; split += ds; h += dh; b += db;
+        if (qt >= p.qtiles) { qt -= p.qtiles; ++split; }
         if (split >= p.splits) { split -= p.splits; ++h; }
         if (h >= a.Hq) { h -= a.Hq; ++b; }
         if (item < p.items) derive(a, p);
+        return item < p.items;
     }
 };
-
-// Tiles that half h takes of an item (0: the half sits it out).
-__device__ __forceinline__ int half_tiles(const CrossArgs& a, const Plan& p, const Work& w, int h) {
-    if (p.solo) return (w.T + 1 - h) / 2;
-    return w.q0 + h * BM < a.Nq ? w.T : 0;
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -132,34 +123,38 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
                        float* __restrict__ o_part, float* __restrict__ lse_part,
                        int* __restrict__ err, int* __restrict__ lost) {
     constexpr uint32_t kTile = (D / 64) * 16384;
-    constexpr int NS = ring_slots<D>();
+    constexpr int NK = k_slots<D>(), NV = v_slots<D>();
     if (tc::refuse_start(lost, err)) return;
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ Shared sh;
-    const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t sQ = base, sRing = base + 2 * kTile, sStage = sRing + NS * kTile;
+    const uint32_t base = tc::smem_u32(smem_raw);   // 1024-byte aligned: see launch()
+    const uint32_t sQ = base, sK = sQ + 2 * kTile, sV = sK + NK * kTile;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        for (int h = 0; h < 2; ++h) {
-            tc::mbar_init(tc::smem_u32(&sh.q_full[h]), 1);
-            tc::mbar_init(tc::smem_u32(&sh.q_empty[h]), 1);
-            tc::mbar_init(tc::smem_u32(&sh.s_full[h]), 1);
-            tc::mbar_init(tc::smem_u32(&sh.p_full[h]), 4);
-            tc::mbar_init(tc::smem_u32(&sh.o_full[h]), 1);
-            tc::mbar_init(tc::smem_u32(&sh.o_free[h]), 4);
-            tc::mbar_init(tc::smem_u32(&sh.turn[h]), 4);
-            tc::mbar_init(tc::smem_u32(&sh.drain[h]), 1);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(tc::smem_u32(&sh.q_full[i]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.q_empty[i]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.p_full[i]), 8);
+            tc::mbar_init(tc::smem_u32(&sh.p_free[i]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.drain[i]), 1);
         }
-        for (int s = 0; s < NS; ++s) {
-            tc::mbar_init(tc::smem_u32(&sh.full[s]), 1);
-            tc::mbar_init(tc::smem_u32(&sh.empty[s]), 2);
+        for (int i = 0; i < 4; ++i) {
+            tc::mbar_init(tc::smem_u32(&sh.k_full[i]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.k_empty[i]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.v_full[i]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.v_empty[i]), 1);
         }
+        tc::mbar_init(tc::smem_u32(&sh.s_full), 1);
+        tc::mbar_init(tc::smem_u32(&sh.s_read), 8);
+        tc::mbar_init(tc::smem_u32(&sh.o_full), 1);
+        tc::mbar_init(tc::smem_u32(&sh.o_free), 4);
+        tc::mbar_init(tc::smem_u32(&sh.ml_full), 8);
         sh.abort_flag = 0;
         sh.keep_tmem = 0;
         tc::mbar_init_fence();
     }
-    if (warp == kMmaWarp) {
+    if (warp == kQkWarp) {
         tc::tmem_alloc(tc::smem_u32(&sh.tmem_base), kTmemCols);
         tc::tmem_relinquish();
     }
@@ -168,191 +163,115 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
     tc::fence_after_sync();
     const uint32_t tmem = sh.tmem_base;
     volatile int* abort_flag = &sh.abort_flag;
+    Work w;
 
-    if (warp >= 8) {
-        tc::regs_dec<kIssueRegs>();
-        if (warp == kProducerWarp && lane == 0) {
-            // -------------------------------------------------------- producer
-            Ring ring;
-            uint32_t fills = 0;          // slots filled so far
-            uint32_t used[2] = {0, 0};   // Q tiles loaded per half
-            bool ok = true;
-            Work w;
-            for (w.start(a, plan); ok && w.item < plan.items; w.next(a, plan)) {
-                for (int h = 0; ok && h < 2; ++h) {
-                    if (half_tiles(a, plan, w, h) == 0) continue;
-                    if (used[h] > 0 &&
-                        !poll_bar(&sh.q_empty[h], (used[h] - 1) & 1, abort_flag, err, (1 << 16) + h)) {
-                        ok = false;
-                        break;
-                    }
-                    load_tile<D>(maps.q, sQ + h * kTile, w.b, w.h, w.q0 + (plan.solo ? 0 : h * BM),
-                                 tc::smem_u32(&sh.q_full[h]));
-                    ++used[h];
-                }
-                // the next item's query rows on their way from HBM to L2 meanwhile
-                if (ok && w.item + (int)gridDim.x < plan.items) {
-                    Work x = w;
-                    x.next(a, plan);
-                    for (int h = 0; h < 2; ++h)
-                        if (half_tiles(a, plan, x, h) > 0 && !(plan.solo && h))
-                            prefetch_tile<D>(maps.q, x.b, x.h, x.q0 + h * BM);
-                }
-                for (int j = 0; ok && j < 2 * w.T; ++j) {
-                    if (fills >= NS &&
-                        !poll_bar(&sh.empty[ring.slot], ring.phase ^ 1, abort_flag, err, (2 << 16) + j)) {
-                        ok = false;
-                        break;
-                    }
-                    load_key_tile<D>((j & 1) ? maps.v : maps.k, sRing + ring.slot * kTile, w.b, w.hk,
-                                     (w.t0 + (j >> 1)) * BN, w.keys, a.Nk, tc::smem_u32(&sh.full[ring.slot]));
-                    ++fills;
-                    ring.next(NS);
-                }
-            }
-            // gave up: let the copies in flight land before the CTA ends
-            if (!ok) {
-                for (int h = 0; h < 2; ++h)
-                    if (used[h] > 0) tc::drain_bar(&sh.q_full[h], (used[h] - 1) & 1);
-                for (uint32_t f = fills > NS ? fills - NS : 0; f < fills; ++f)
-                    tc::drain_bar(&sh.full[f % NS], (f / NS) & 1);
-            }
-        } else if ((warp == kMmaWarp || warp == kMmaWarp + 1) && lane == 0) {
-            // ------------------------------------------------------- MMA issue
-            const int h = warp - kMmaWarp;
-            const uint32_t tS = tmem + h * BN, tO = tmem + 2 * BN + h * D;
-            Ring ring;
-            uint32_t n = 0, tiles = 0;   // items and tiles of this half so far
-            bool ok = true;
-            auto skip_slot = [&]() {
-                ok = poll_bar(&sh.full[ring.slot], ring.phase, abort_flag, err, (3 << 16) + h);
-                if (ok) tc::mbar_arrive(tc::smem_u32(&sh.empty[ring.slot]));
-                ring.next(NS);
-            };
-            Work w;
-            for (w.start(a, plan); ok && w.item < plan.items; w.next(a, plan)) {
-                const int mine = half_tiles(a, plan, w, h);
-                int j = 0;   // tile of the ring position
-                // passes the tiles of the other half
-                auto skip_to = [&](int t) {
-                    for (; ok && j < t; ++j) {
-                        skip_slot();
-                        if (ok) skip_slot();
-                    }
-                };
-                if (mine == 0) {
-                    skip_to(w.T);
-                    continue;
-                }
-                const int step = plan.solo ? 2 : 1;
-                const bool solo = plan.solo != 0;
-                skip_to(solo ? h : 0);
-                ok = ok && poll_bar(&sh.q_full[h], n & 1, abort_flag, err, (4 << 16) + h) &&
-                     poll_bar(&sh.full[ring.slot], ring.phase, abort_flag, err, (5 << 16));
-                if (!ok) break;
-                tc::fence_after_sync();
-                mma_dot<D>(tS, sQ + h * kTile, sRing + ring.slot * kTile);
-                tc::commit(tc::smem_u32(&sh.s_full[h]));
-                tc::commit(tc::smem_u32(&sh.empty[ring.slot]));
-                if (mine == 1) tc::commit(tc::smem_u32(&sh.q_empty[h]));
-                ring.next(NS);
-                for (int i = 0; i < mine; ++i) {
-                    // everything the next two products need but P is waited
-                    // for ahead of it, so that PV and the next QK follow P
-                    // without a pause.  (The ring holds what this waits for:
-                    // V, the other half's K and V when solo, the next K.)
-                    const int vslot = ring.slot;
-                    if (!(ok = poll_bar(&sh.full[vslot], ring.phase, abort_flag, err, (8 << 16) + i))) break;
-                    ring.next(NS);
-                    ++j;
-                    const bool more = i + 1 < mine;
-                    if (more) {
-                        skip_to(j + step - 1);
-                        if (!ok || !(ok = poll_bar(&sh.full[ring.slot], ring.phase, abort_flag, err, (5 << 16) + i)))
-                            break;
-                    }
-                    // the first PV overwrites O: the last item's must be read out
-                    if (i == 0 && n > 0 &&
-                        !(ok = poll_bar(&sh.o_free[h], (n - 1) & 1, abort_flag, err, (7 << 16) + h)))
-                        break;
-                    if (!(ok = poll_bar(&sh.p_full[h], tiles & 1, abort_flag, err, (6 << 16) + i))) break;
-                    ++tiles;
-                    tc::fence_after_sync();
-                    mma_rows<D>(tO, tS, sRing + vslot * kTile, i > 0 ? 1u : 0u);
-                    if (more) {
-                        mma_dot<D>(tS, sQ + h * kTile, sRing + ring.slot * kTile);
-                        tc::commit(tc::smem_u32(&sh.s_full[h]));
-                        tc::commit(tc::smem_u32(&sh.empty[vslot]));
-                        tc::commit(tc::smem_u32(&sh.empty[ring.slot]));
-                        if (i + 2 == mine) tc::commit(tc::smem_u32(&sh.q_empty[h]));
-                        ring.next(NS);
-                    } else {
-                        tc::commit(tc::smem_u32(&sh.o_full[h]));
-                        tc::commit(tc::smem_u32(&sh.empty[vslot]));
-                    }
-                }
-                if (!ok) break;
-                skip_to(w.T);
+    if ((warp == kLoadWarp || warp == kVWarp) && lane == 0) {
+        // ----------------------------------------------------------- producers
+        // (of Q and K, and of V: one for both would hold up K behind a V slot)
+        const bool is_k = warp == kLoadWarp;
+        const int NS = is_k ? NK : NV;
+        uint64_t* full = is_k ? sh.k_full : sh.v_full;
+        uint64_t* empty = is_k ? sh.k_empty : sh.v_empty;
+        const RowMaps& map = is_k ? maps.k : maps.v;
+        const uint32_t slots = is_k ? sK : sV;
+        Ring ring;
+        uint32_t fills = 0, n = 0;
+        bool ok = true;
+        for (bool more = w.start(a, plan); ok && more; more = w.next(a, plan)) {
+            if (w.T == 0) continue;
+            if (is_k) {
+                const int s = n & 1;
+                if (n >= 2 && !(ok = poll_bar(&sh.q_empty[s], ((n >> 1) - 1) & 1, abort_flag, err, (1 << 16)))) break;
+                load_tile<D>(maps.q, sQ + s * kTile, w.b, w.h, w.qt * BM, tc::smem_u32(&sh.q_full[s]));
                 ++n;
+                // a coming item's rows on their way from HBM to L2
+                Work x = w;
+                if (x.next(a, plan) && x.next(a, plan) && x.T > 0) prefetch_tile<D>(maps.q, x.b, x.h, x.qt * BM);
             }
-            // every MMA of this thread is complete once its drain flips; if
-            // that wait expires TMEM stays allocated and the device's lost
-            // word stops every later tensor-core kernel before it allocates
-            tc::commit(tc::smem_u32(&sh.drain[h]));
-            if (!tc::drain_bar(&sh.drain[h], 0)) {
-                sh.keep_tmem = 1;
-                tc::mark_tmem_lost(lost);
-                if (atomicCAS(err, 0, SVGEAR_ERR_TIMEOUT) == 0) {
-                    err[1] = (9 << 16) + h;
-                    err[2] = blockIdx.x;
-                }
+            for (int j = 0; j < w.T; ++j) {
+                if (fills >= (uint32_t)NS && !(ok = poll_bar(&empty[ring.slot], ring.phase ^ 1, abort_flag, err, (2 << 16))))
+                    break;
+                load_key_tile<D>(map, slots + ring.slot * kTile, w.b, w.hk, (w.t0 + j) * BN, w.keys, a.Nk,
+                                 tc::smem_u32(&full[ring.slot]));
+                ++fills;
+                ring.next(NS);
             }
         }
-        __syncwarp();
-    } else {
-        tc::regs_inc<kSoftmaxRegs>();
+        // gave up: let the copies in flight land before the CTA ends
+        if (!ok) {
+            for (uint32_t q = n > 2 ? n - 2 : 0; q < n; ++q) tc::drain_bar(&sh.q_full[q & 1], (q >> 1) & 1);
+            for (uint32_t f = fills > (uint32_t)NS ? fills - NS : 0; f < fills; ++f)
+                tc::drain_bar(&full[f % NS], (f / NS) & 1);
+        }
+    } else if ((warp == kQkWarp || warp == kPvWarp) && lane == 0) {
+        // ----------------------------------------------------------- MMA issue
+        const bool qk = warp == kQkWarp;
+        Ring ring;
+        uint32_t n = 0, g = 0;
+        bool ok = true;
+        for (bool more = w.start(a, plan); ok && more; more = w.next(a, plan)) {
+            if (w.T == 0) continue;
+            if (qk) {
+                ok = poll_bar(&sh.q_full[n & 1], (n >> 1) & 1, abort_flag, err, (4 << 16));
+                for (int j = 0; ok && j < w.T; ++j, ++g) {
+                    // S(g) overwrites S(g - 1), which must be in registers
+                    if (!(ok = poll_bar(&sh.k_full[ring.slot], ring.phase, abort_flag, err, (5 << 16)) &&
+                               (g == 0 || poll_bar(&sh.s_read, (g - 1) & 1, abort_flag, err, (6 << 16)))))
+                        break;
+                    tc::fence_after_sync();
+                    mma_dot<D>(tmem, sQ + (n & 1) * kTile, sK + ring.slot * kTile);
+                    tc::commit(tc::smem_u32(&sh.s_full));
+                    tc::commit(tc::smem_u32(&sh.k_empty[ring.slot]));
+                    ring.next(NK);
+                }
+                if (ok) tc::commit(tc::smem_u32(&sh.q_empty[n & 1]));
+            } else {
+                // the first PV overwrites O: the last item's must be read out
+                ok = n == 0 || poll_bar(&sh.o_free, (n - 1) & 1, abort_flag, err, (4 << 16) + 1);
+                for (int j = 0; ok && j < w.T; ++j, ++g) {
+                    const uint32_t b = g & 1;
+                    if (!(ok = poll_bar(&sh.v_full[ring.slot], ring.phase, abort_flag, err, (7 << 16)) &&
+                               poll_bar(&sh.p_full[b], (g >> 1) & 1, abort_flag, err, (8 << 16))))
+                        break;
+                    tc::fence_after_sync();
+                    const uint32_t tile = sV + ring.slot * kTile, tP = tmem + kP + b * HN, acc = j > 0 ? 1u : 0u;
+                    mma_rows_k64<D>(tmem + kO, tP, tile, acc);
+                    mma_rows_k64<D>(tmem + kO + D, tP + 32, tile + HN * 128, acc);
+                    tc::commit(tc::smem_u32(&sh.p_free[b]));
+                    tc::commit(tc::smem_u32(&sh.v_empty[ring.slot]));
+                    ring.next(NV);
+                }
+                if (ok) tc::commit(tc::smem_u32(&sh.o_full));
+            }
+            ++n;
+        }
+        drain_mma(&sh.drain[qk ? 0 : 1], &sh.keep_tmem, err, lost, (9 << 16) + (qk ? 0 : 1));
+    } else if (warp < 8) {
         // -------------------------------------------------------------- softmax
         const int h = warp >> 2, r = tid & 127;
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t tS = lane_base + h * BN, tO = lane_base + 2 * BN + h * D;
-        uint32_t n = 0, tiles = 0, turns = 0;
+        const uint32_t tS = lane_base + h * HN, tO = lane_base + kO + h * D;
+        uint32_t n = 0, g = 0;
         bool ok = true;
-        uint32_t v[BN];
-        Work w;
-        for (w.start(a, plan); ok && w.item < plan.items; w.next(a, plan)) {
-            const int mine = half_tiles(a, plan, w, h);
-            const int paired = min(mine, half_tiles(a, plan, w, 1 - h));
-            const int row = w.q0 + (plan.solo ? 0 : h * BM) + r;
+        for (bool more = w.start(a, plan); ok && more; more = w.next(a, plan)) {
+            if (w.T == 0) continue;
             float m_use = -INFINITY, l = 0.f;
-            for (int i = 0; i < mine; ++i) {
-                if (!(ok = warp_poll_bar(&sh.s_full[h], tiles & 1, abort_flag, err, (10 << 16) + i))) break;
-                ++tiles;
+            for (int j = 0; j < w.T; ++j, ++g) {
+                const uint32_t b = g & 1, tP = lane_base + kP + b * HN + h * 32;
+                if (!(ok = warp_poll_bar(&sh.s_full, g & 1, abort_flag, err, (10 << 16)))) break;
                 tc::fence_after_sync();
-                const int j = w.t0 + (plan.solo ? 2 * i + h : i);
-                const int valid = w.keys - j * BN;
-                if (valid < BN) {
-                    // the batch's last tile: -inf past the keys, rewritten in
-                    // TMEM so that the main path carries no selects
-#pragma unroll 1
-                    for (int c4 = valid / 32; c4 < BN / 32; ++c4) {
-                        uint32_t t[32];
-                        tc::tmem_ld32(tS + c4 * 32, t);
-                        tc::tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (c4 * 32 + e >= valid) t[e] = __float_as_uint(-INFINITY);
-                        tc::tmem_st32(tS + c4 * 32, t);
-                    }
-                    tc::tmem_st_wait();
-                }
-                tc::tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+                const int valid = w.keys - (w.t0 + j) * BN - h * HN;   // of this half
+                if (valid < HN) mask_columns<HN>(tS, valid);
+                uint32_t v[HN];
+                tc::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
                 tc::tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
-                tc::tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&v[64]));
-                tc::tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&v[96]));
                 tc::tmem_ld_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.s_read));
                 float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < BN; e += 8) {
+                for (int e = 0; e < HN; e += 8) {
                     mx0 = fmax3(mx0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
                     mx1 = fmax3(mx1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
                     mx2 = fmax3(mx2, __uint_as_float(v[e + 4]), __uint_as_float(v[e + 5]));
@@ -361,32 +280,24 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
                 const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * scale_log2;   // scale > 0
                 const float m_new = fmaxf(m_use, mx);
                 // O is rescaled only when a row's maximum grows by more than
-                // 2^8 (the weights then stay below 2^8, far from bf16's and
-                // fp32's ranges); TMEM accesses are warp-collective, so the
-                // warp rescales together.  s_full came with the commit after
-                // the previous PV, so O is complete here.
-                const bool need = i > 0 && m_new > m_use + kRescaleThreshold;
+                // 2^8 (the weights then stay below 2^8, far from the ends of
+                // bf16 and fp32); TMEM accesses are warp-collective, so the
+                // warp rescales together.
+                const bool need = j > 0 && m_new > m_use + kRescaleThreshold;
                 const bool any = __any_sync(0xffffffffu, need);
                 float alpha = 1.f;
-                if (i == 0) {
+                if (j == 0) {
                     m_use = m_new;
                 } else if (need) {
                     alpha = tc::ex2(m_use - m_new);
                     l *= alpha;
                     m_use = m_new;
                 }
-                const float neg_m = m_use == -INFINITY ? 0.f : -m_use;   // every score -inf so far
-                // the halves take turns on the exp unit
-                if (i < paired) {
-                    if ((h == 1 || turns > 0) &&
-                        !(ok = warp_poll_bar(&sh.turn[h], (turns - 1 + h) & 1, abort_flag, err, (12 << 16) + i)))
-                        break;
-                    ++turns;
-                }
+                const float neg_m = m_use == -INFINITY ? 0.f : -m_use;   // no finite score so far
                 uint64_t s01 = 0ull;
                 const uint64_t xs2 = pack2(scale_log2, scale_log2), nm2 = pack2(neg_m, neg_m);
 #pragma unroll
-                for (int q = 0; q < BN / 32; ++q) {
+                for (int q = 0; q < HN / 32; ++q) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
@@ -397,12 +308,17 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
                         add2(s01, p0, p1);
                         pk[e >> 1] = bf16_pair(p0, p1);
                     }
-                    tc::tmem_st16(tS + q * 16, pk);
-                    if (q == kTurnChunk && i < paired && lane == 0)
-                        tc::mbar_arrive(tc::smem_u32(&sh.turn[1 - h]));
+                    // P(g - 2) must have been read out of the buffer
+                    if (q == 0 && g >= 2)
+                        ok = warp_poll_bar(&sh.p_free[b], ((g >> 1) - 1) & 1, abort_flag, err, (11 << 16));
+                    tc::tmem_st16(tP + q * 16, pk);
                 }
+                if (!ok) break;
                 l += __uint_as_float((uint32_t)s01) + __uint_as_float((uint32_t)(s01 >> 32));
                 if (any) {
+                    // PV(g - 1), the last addition to O_h, must be complete
+                    if (!(ok = warp_poll_bar(&sh.p_free[b ^ 1], ((g - 1) >> 1) & 1, abort_flag, err, (12 << 16)))) break;
+                    tc::fence_after_sync();
                     uint32_t o[16];
 #pragma unroll 1
                     for (int c = 0; c < D / 16; ++c) {
@@ -416,87 +332,109 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
                 tc::tmem_st_wait();
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.p_full[h]));
+                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.p_full[b]));
             }
             if (!ok) break;
-            if (mine > 0) {
-                if (!(ok = warp_poll_bar(&sh.o_full[h], n & 1, abort_flag, err, (11 << 16)))) break;
+            // (the epilogue must have read the last item's pair)
+            if (n > 0 && !(ok = warp_poll_bar(&sh.o_free, (n - 1) & 1, abort_flag, err, (14 << 16)))) break;
+            sh.ml[h][r] = make_float2(m_use, l);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.ml_full));
+            ++n;
+        }
+    } else if (warp >= kEpilogueWarp) {
+        // ------------------------------------------------------------- epilogue
+        // o = (a_0 O_0 + a_1 O_1) / (a_0 l_0 + a_1 l_1), a_h = 2^(m_h - m)
+        const int r = tid & 127;
+        const uint32_t tO = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kO;
+        const bool parts = plan.splits > 1;
+        uint32_t n = 0;
+        for (bool more = w.start(a, plan); more; more = w.next(a, plan)) {
+            const int row = w.qt * BM + r;
+            const bool write = row < a.Nq;
+            const size_t rr = ((size_t)w.b * a.Hq + w.h) * a.Nq + row;
+            const size_t part = (size_t)w.split * a.B * a.Hq * a.Nq + rr;
+            float sum = 0.f, m = 0.f, c0 = 0.f, c1 = 0.f;
+            if (w.T > 0) {
+                if (!warp_poll_bar(&sh.ml_full, n & 1, abort_flag, err, (13 << 16))) break;
+                const float2 x0 = sh.ml[0][r], x1 = sh.ml[1][r];
+                m = fmaxf(x0.x, x1.x);
+                const float mu = m == -INFINITY ? 0.f : m;   // no finite score
+                c0 = tc::ex2(x0.x - mu);
+                c1 = tc::ex2(x1.x - mu);
+                sum = fmaf(c0, x0.y, c1 * x1.y);
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                c0 *= inv;
+                c1 *= inv;
+                if (!warp_poll_bar(&sh.o_full, n & 1, abort_flag, err, (15 << 16))) break;
                 tc::fence_after_sync();
                 ++n;
             }
-            // epilogue; an item without tiles leaves zeros and lse = -inf
-            const bool write = row < a.Nq;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            const float lse = l == 0.f ? -INFINITY : fmaf(m_use, 0.6931471805599453f, logf(l));
-            const size_t rr = ((size_t)w.b * a.Hq + w.h) * a.Nq + row;
-            const bool parts = plan.splits > 1 || plan.solo;
-            const size_t part = (size_t)(plan.solo ? 2 * w.split + h : w.split) * a.B * a.Hq * a.Nq + rr;
+            // 32 columns of both accumulators at a time (beside running MMAs a
+            // TMEM load takes some 350 cycles whatever its size) in a rolled
+            // loop (this code runs once per item, fetched anew each time)
+            bf16* dst = row_ptr<bf16>(a.O, w.b, w.h, row - lane);
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o0[32], o1[32];
+                if (w.T > 0) {
+                    tc::tmem_ld32(tO + c * 32, o0);
+                    tc::tmem_ld32(tO + D + c * 32, o1);
+                    tc::tmem_ld_wait();
+                    if (c == D / 32 - 1) {   // the accumulators and the pair have been read
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.o_free));
+                    }
+                }
+                if (w.T > 0) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        uint32_t y0, y1;
+                        fma2(o1[e], o1[e + 1], pack2(c1, c1), 0ull, y0, y1);
+                        fma2(o0[e], o0[e + 1], pack2(c0, c0), (uint64_t)y0 | ((uint64_t)y1 << 32), o0[e], o0[e + 1]);
+                    }
+                } else {   // no key
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o0[e] = 0;
+                }
+                if (parts) {
+                    if (write && w.T > 0) {
+                        uint4* o4 = reinterpret_cast<uint4*>(o_part + part * D + c * 32);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            o4[q] = make_uint4(o0[4 * q], o0[4 * q + 1], o0[4 * q + 2], o0[4 * q + 3]);
+                    }
+                } else {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        pk[e] = bf16_pair(__uint_as_float(o0[2 * e]), __uint_as_float(o0[2 * e + 1]));
+                    store_rows32(dst + c * 32, a.O.stride_n, a.Nq - (row - lane), lane, pk);
+                }
+            }
             if (write) {
+                const float lse = sum == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(sum));
                 if (parts) lse_part[part] = lse;
                 else a.lse[rr] = lse;
             }
-            auto free_o = [&]() {
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.o_free[h]));
-            };
-            if (mine == 0) {
-                if (write && !parts) {
-                    uint4* o4 = reinterpret_cast<uint4*>(row_ptr<bf16>(a.O, w.b, w.h, row));
-#pragma unroll 1
-                    for (int c = 0; c < D / 8; ++c) o4[c] = make_uint4(0, 0, 0, 0);
-                }
-            } else if (parts) {
-                uint32_t o[32];
-#pragma unroll 1
-                for (int c4 = 0; c4 < D / 32; ++c4) {
-                    tc::tmem_ld32(tO + c4 * 32, o);
-                    tc::tmem_ld_wait();
-                    if (write) {
-                        float4* o4 = reinterpret_cast<float4*>(o_part + part * D + c4 * 32);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            o4[q] = make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
-                                                __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
-                    }
-                }
-                free_o();
-            } else {
-                const int n0 = row - lane;
-                uint32_t o[D];
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c)
-                    tc::tmem_ld32(tO + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[c * 32]));
-                tc::tmem_ld_wait();
-                free_o();
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        pk[e] = bf16_pair(__uint_as_float(o[c * 64 + 2 * e]) * inv, __uint_as_float(o[c * 64 + 2 * e + 1]) * inv);
-                    store_rows<0>(maps.o, sStage + warp * 4096, pk, c * 64, w.b, w.h, n0, n0 < a.Nq, lane);
-                }
-            }
         }
-        if (lane == 0) tc::bulk_wait_read<0>();   // shared memory outlives its stores
-        __syncwarp();
     }
+    __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == kMmaWarp && !sh.keep_tmem) tc::tmem_dealloc(tmem, kTmemCols);
+    if (warp == kQkWarp && !sh.keep_tmem) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
 Plan make_plan(int B, int Hq, int Nq, int Nk) {
     Plan p;
-    p.qpairs = ceil_div(Nq, 2 * BM);
+    p.qtiles = ceil_div(Nq, BM);
     const int key_tiles = ceil_div(Nk, BN);
-    const CrossSplit s = cross_split((long long)B * Hq * p.qpairs, key_tiles, kSms, 2);
+    const CrossSplit s = cross_split((long long)B * Hq * p.qtiles, key_tiles, kSms, kMinSplitTiles);
     p.splits = s.splits;
     p.tiles = s.tiles;
-    p.solo = Nq <= BM && p.tiles >= 2;
-    p.items = B * Hq * p.qpairs * p.splits;
+    p.items = B * Hq * p.qtiles * p.splits;
     return p;
 }
 
@@ -504,22 +442,14 @@ template <int D>
 int launch(const CrossArgs& a, const Plan& plan, float* o_part, float* lse_part, int* err, int* lost,
            cudaStream_t st) {
     const void* fn = (const void*)cross_fwd_sm100_kernel<D>;
-    static int launch_regs = 0;
-    if (launch_regs == 0) {
-        cudaFuncAttributes fa;
-        if (cudaFuncGetAttributes(&fa, fn) != cudaSuccess) return SVGEAR_ERR_CUDA;
-        launch_regs = fa.numRegs;
-    }
-    if (launch_regs < kMinLaunchRegs) return SVGEAR_ERR_UNSUPPORTED;
     Maps maps;
-    if (!make_tile_map(&maps.q, a.Q, a.B, a.Hq, a.Nq, D) || !make_tile_map(&maps.o, a.O, a.B, a.Hq, a.Nq, D, 32) ||
-        !make_row_maps(&maps.k, a.K, a.B, a.Hkv, a.Nk, D, a.k_len != nullptr) ||
-        !make_row_maps(&maps.v, a.V, a.B, a.Hkv, a.Nk, D, a.k_len != nullptr))
+    const bool pieces = a.k_len != nullptr;
+    if (!make_tile_map(&maps.q, a.Q, a.B, a.Hq, a.Nq, D, BM) ||
+        !make_row_maps(&maps.k, a.K, a.B, a.Hkv, a.Nk, D, pieces) ||
+        !make_row_maps(&maps.v, a.V, a.B, a.Hkv, a.Nk, D, pieces))
         return SVGEAR_ERR_CUDA;
-    const size_t smem = (size_t)(2 + ring_slots<D>()) * (D / 64) * 16384 + 8 * 4096 + 1024;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return SVGEAR_ERR_CUDA;
-    cross_fwd_sm100_kernel<D><<<plan.items < kSms ? plan.items : kSms, kThreads, smem, st>>>(
+    if (int s = set_aligned_smem(fn, smem_bytes<D>())) return s;
+    cross_fwd_sm100_kernel<D><<<plan.items < kSms ? plan.items : kSms, kThreads, smem_bytes<D>(), st>>>(
         maps, a, plan, a.scale * 1.4426950408889634f, o_part, lse_part, err, lost);
     count_launches(1);
     SVGEAR_LAUNCH_CHECK();
@@ -530,8 +460,7 @@ int launch(const CrossArgs& a, const Plan& plan, float* o_part, float* lse_part,
 }  // namespace crosstc
 
 int cross_sm100_parts(int B, int Hq, int Nq, int Nk) {
-    const crosstc::Plan p = crosstc::make_plan(B, Hq, Nq, Nk);
-    return p.solo ? 2 * p.splits : p.splits;
+    return crosstc::make_plan(B, Hq, Nq, Nk).splits;
 }
 
 int launch_cross_sm100(const CrossArgs& a, float* o_part, float* lse_part, int* err, cudaStream_t st) {

@@ -99,28 +99,37 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Stores 64 bf16 columns [col0, col0 + 64) of 32 rows, one row per lane (packed
-// pairs pk), to rows n0.. of head (b, h): through a 4 KB staging area of the
-// warp (128-byte swizzle) and a TMA store, so that whole lines reach L2 (each
-// lane storing its own row would touch 32 lines per instruction).  A warp with
-// PENDING + 1 areas uses them in turn.  `map` has boxes of 32 rows; rows past
-// the tensor are left out.
-template <int PENDING>
-__device__ __forceinline__ void store_rows(const TileMap& map, uint32_t area, const uint32_t (&pk)[32], int col0,
-                                           int b, int h, int n0, bool any_row, int lane) {
-    if (lane == 0) tc::bulk_wait_read<PENDING>();   // this area's last store has been read
-    __syncwarp();
+// Stores 32 bf16 columns of the warp's 32 rows, one row per lane in packed pairs
+// (pk), first row `row0` of `rows`, at base + row * stride (elements).  The four
+// lanes of a quad transpose their 16-byte pieces, so that a store instruction
+// writes 64 contiguous bytes of eight rows instead of 16 bytes of 32.
+__device__ __forceinline__ void store_rows32(__nv_bfloat16* base, int64_t stride, int rows, int lane,
+                                             uint32_t (&pk)[16]) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(area + lane * 128 + ((c ^ (lane & 7)) << 4)),
-                     "r"(pk[4 * c]), "r"(pk[4 * c + 1]), "r"(pk[4 * c + 2]), "r"(pk[4 * c + 3])
-                     : "memory");
-    tc::fence_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-        if (any_row) tc::tma_store_4d(&map.box, area, col0, n0, h * map.hmul, b * map.bmul);
-        tc::bulk_commit();
+    for (int w = 0; w < 4; ++w) {
+        // words w of pieces (0, 1) and (2, 3) change places with lane ^ 2, then of
+        // (0, 2) and (1, 3) with lane ^ 1
+        const bool up2 = lane & 2, up1 = lane & 1;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t &x = pk[4 * j + w], &y = pk[4 * (j + 2) + w];
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, up2 ? x : y, 2);
+            if (up2) x = got; else y = got;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            uint32_t &x = pk[4 * j + w], &y = pk[4 * (j + 1) + w];
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, up1 ? x : y, 1);
+            if (up1) x = got; else y = got;
+        }
     }
+    const int r0 = lane & ~3;
+    __nv_bfloat16* dst = base + (lane & 3) * 8;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+        if (r0 + t < rows)
+            *reinterpret_cast<uint4*>(dst + (r0 + t) * stride) =
+                make_uint4(pk[4 * t], pk[4 * t + 1], pk[4 * t + 2], pk[4 * t + 3]);
 }
 
 // S (128 x 128) = A B^T over D, both K-major tiles in shared memory.
@@ -136,17 +145,16 @@ __device__ __forceinline__ void mma_dot(uint32_t d_tmem, uint32_t sA, uint32_t s
                          tc::sw128_desc(sB + ks * 32, 16, 1024), kIdesc, ks > 0);
     }
 }
-// O (128 x D) (+)= P X: P (128 x 128 bf16) in tensor memory, X a row tile in
-// shared memory read MN-major.
+// O (128 x D) (+)= P X over 64 rows of X: P (128 x 64 bf16) in 32 columns of
+// tensor memory, X rows of a tile in shared memory, read MN-major.
 template <int D>
-__device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a_tmem, uint32_t sX,
-                                         uint32_t accumulate) {
-    tc::mma_bf16_ts_k128(d_tmem, a_tmem, tc::sw128_desc(sX, 16384, 1024), tc::idesc_bf16(BM, D, true),
-                         accumulate);
+__device__ __forceinline__ void mma_rows_k64(uint32_t d_tmem, uint32_t a_tmem, uint32_t sX,
+                                             uint32_t accumulate) {
+    tc::mma_bf16_ts_k64(d_tmem, a_tmem, tc::sw128_desc(sX, 16384, 1024), tc::idesc_bf16(BM, D, true),
+                        accumulate);
 }
-
-// The same with P in two runs of 32 columns, 64 columns apart (each warpgroup's
-// half over the first columns of its scores).
+// The same over 128 rows, P in two runs of 32 columns, 64 columns apart (each
+// warpgroup's half over the first columns of its scores).
 template <int D>
 __device__ __forceinline__ void mma_rows_2x64(uint32_t d_tmem, uint32_t a_tmem, uint32_t sX,
                                               uint32_t accumulate) {
@@ -173,6 +181,50 @@ __device__ __forceinline__ void fma2(uint32_t x0, uint32_t x1, uint64_t m, uint6
 __device__ __forceinline__ void add2(uint64_t& s, float p0, float p1) {
     asm("{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\tadd.rn.f32x2 %0, %0, x;\n\t}"
         : "+l"(s) : "f"(p0), "f"(p1));
+}
+
+// One thread's MMAs are complete once `bar` flips; if that wait expires TMEM
+// stays allocated and the device's lost word stops every later tensor-core
+// kernel before it allocates.
+__device__ __forceinline__ void drain_mma(uint64_t* bar, int* keep_tmem, int* err, int* lost, int where) {
+    tc::commit(tc::smem_u32(bar));
+    if (!tc::drain_bar(bar, 0)) {
+        *keep_tmem = 1;
+        tc::mark_tmem_lost(lost);
+        if (atomicCAS(err, 0, SVGEAR_ERR_TIMEOUT) == 0) {
+            err[1] = where;
+            err[2] = blockIdx.x;
+        }
+    }
+}
+
+// Rewrites columns >= valid of this warp's N score columns at taddr to -inf: in
+// TMEM, so that the main path carries no selects.
+template <int N>
+__device__ __forceinline__ void mask_columns(uint32_t taddr, int valid) {
+#pragma unroll 1
+    for (int c4 = max(valid, 0) / 32; c4 < N / 32; ++c4) {
+        uint32_t t[32];
+        tc::tmem_ld32(taddr + c4 * 32, t);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (c4 * 32 + e >= valid) t[e] = __float_as_uint(-INFINITY);
+        tc::tmem_st32(taddr + c4 * 32, t);
+    }
+    tc::tmem_st_wait();
+}
+
+// Dynamic shared memory of a kernel whose tiles fill it: the 128-byte swizzle
+// needs 1024-byte aligned tiles, and the dynamic part starts after the static
+// one, which is padded to a multiple of that.
+inline int set_aligned_smem(const void* fn, uint32_t bytes) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, fn) != cudaSuccess) return SVGEAR_ERR_CUDA;
+    if (fa.sharedSizeBytes % 1024 != 0) return SVGEAR_ERR_UNSUPPORTED;
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess
+               ? SVGEAR_OK
+               : SVGEAR_ERR_CUDA;
 }
 
 // A slot ring's position: slot index and the parity of its current use.

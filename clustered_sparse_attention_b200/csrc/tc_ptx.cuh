@@ -157,25 +157,6 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const void* tmap, int 
         : "memory");
 }
 
-// Writes the tensor map's box from shared memory to (x, y, z, w); rows past the
-// tensor are left out.  Part of the issuing thread's current bulk group.
-__device__ __forceinline__ void tma_store_4d(const void* tmap, uint32_t src, int x, int y, int z,
-                                             int w) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
-            reinterpret_cast<uint64_t>(tmap)),
-        "r"(x), "r"(y), "r"(z), "r"(w), "r"(src)
-        : "memory");
-}
-__device__ __forceinline__ void bulk_commit() {
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// Until at most N of this thread's bulk groups still read shared memory.
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-
 // ---- tcgen05 ---------------------------------------------------------------
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
@@ -279,6 +260,24 @@ __device__ __forceinline__ void mma_bf16_ts_k128(uint32_t d_tmem, uint32_t a_tme
         "add.u32 t, %1, 48;\n\tadd.s64 b, %2, 768;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
         "add.u32 t, %1, 56;\n\tadd.s64 b, %2, 896;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(1u)
+        : "memory");
+}
+
+// The first four steps of mma_bf16_ts_k128.
+__device__ __forceinline__ void mma_bf16_ts_k64(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                                uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 t;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "add.u32 t, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
+        "add.u32 t, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
+        "add.u32 t, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t}\n" ::"r"(d_tmem),
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(1u)
         : "memory");

@@ -81,15 +81,15 @@ __device__ __forceinline__ bool poll_bar(uint64_t* bar, uint32_t parity, volatil
     uint64_t t0 = 0;
 #pragma unroll 1
     for (uint32_t it = 1;; ++it) {
-        if (mbar_test(b, parity)) return true;
+        if (mbar_try_wait(b, parity)) return true;
         if ((it & 1023) == 0 && !poll_look(&t0, abort_flag, err, where, it)) return false;
     }
 }
+// For a whole warp: every lane polls (one shared-memory access for all, and no
+// divergence to undo), and all get the same answer.
 __device__ __forceinline__ bool warp_poll_bar(uint64_t* bar, uint32_t parity,
                                               volatile int* abort_flag, int* err, int where) {
-    int ok = 0;
-    if ((threadIdx.x & 31) == 0) ok = poll_bar(bar, parity, abort_flag, err, where) ? 1 : 0;
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    return __all_sync(0xffffffffu, poll_bar(bar, parity, abort_flag, err, where)) != 0;
 }
 
 // As wait_bar for copies or MMAs already issued, while a kernel gives up: it
