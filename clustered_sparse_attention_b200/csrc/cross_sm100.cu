@@ -14,7 +14,8 @@
 //   8, 11     TMA producers of Q and K tiles and of V tiles (a ring each);
 //   9, 10     issue S = Q K^T and O_h += P_h V;
 //   12-15     epilogue: merges the two accumulators like partial attentions and
-//             writes the rows, while the softmax is in the next item.
+//             writes the rows, while the softmax is in the next item; they leave
+//             through the item's Q slot, which no product reads any more.
 // TMEM: S | P[0] | P[1] | O_0 | O_1 (128 + 64 + 64 + d + d columns).  Over the
 // CTA's tiles g = 0, 1, ... of all its items, S(g + 1) is issued as soon as the
 // softmax has S(g) in registers and P(g) goes to a buffer of its own, so that
@@ -53,11 +54,11 @@ constexpr uint32_t smem_bytes() { return (2 + k_slots<D>() + v_slots<D>()) * (D 
 
 struct Maps {
     RowMaps k, v;
-    TileMap q;
+    TileMap q, o;   // o: boxes of 32 rows
 };
 
 struct Shared {
-    uint64_t q_full[2], q_empty[2];
+    uint64_t q_full[2], q_free[2];    // Q slot s loaded / its item's output has left it
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
     uint64_t s_full, s_read;
     uint64_t p_full[2], p_free[2];    // P[b] written / read by both PV
@@ -134,7 +135,7 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(tc::smem_u32(&sh.q_full[i]), 1);
-            tc::mbar_init(tc::smem_u32(&sh.q_empty[i]), 1);
+            tc::mbar_init(tc::smem_u32(&sh.q_free[i]), 4);
             tc::mbar_init(tc::smem_u32(&sh.p_full[i]), 8);
             tc::mbar_init(tc::smem_u32(&sh.p_free[i]), 1);
             tc::mbar_init(tc::smem_u32(&sh.drain[i]), 1);
@@ -181,7 +182,7 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
             if (w.T == 0) continue;
             if (is_k) {
                 const int s = n & 1;
-                if (n >= 2 && !(ok = poll_bar(&sh.q_empty[s], ((n >> 1) - 1) & 1, abort_flag, err, (1 << 16)))) break;
+                if (n >= 2 && !(ok = poll_bar(&sh.q_free[s], ((n >> 1) - 1) & 1, abort_flag, err, (1 << 16)))) break;
                 load_tile<D>(maps.q, sQ + s * kTile, w.b, w.h, w.qt * BM, tc::smem_u32(&sh.q_full[s]));
                 ++n;
                 // a coming item's rows on their way from HBM to L2
@@ -224,7 +225,6 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
                     tc::commit(tc::smem_u32(&sh.k_empty[ring.slot]));
                     ring.next(NK);
                 }
-                if (ok) tc::commit(tc::smem_u32(&sh.q_empty[n & 1]));
             } else {
                 // the first PV overwrites O: the last item's must be read out
                 ok = n == 0 || poll_bar(&sh.o_free, (n - 1) & 1, abort_flag, err, (4 << 16) + 1);
@@ -373,7 +373,7 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
             // 32 columns of both accumulators at a time (beside running MMAs a
             // TMEM load takes some 350 cycles whatever its size) in a rolled
             // loop (this code runs once per item, fetched anew each time)
-            bf16* dst = row_ptr<bf16>(a.O, w.b, w.h, row - lane);
+            const uint32_t stage = sQ + ((n - 1) & 1) * kTile;
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o0[32], o1[32];
@@ -410,8 +410,22 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         pk[e] = bf16_pair(__uint_as_float(o0[2 * e]), __uint_as_float(o0[2 * e + 1]));
-                    store_rows32(dst + c * 32, a.O.stride_n, a.Nq - (row - lane), lane, pk);
+                    if (w.T > 0) {
+                        stage_row32(stage, r, c * 32, pk);
+                    } else if (write) {
+                        uint4* o4 = reinterpret_cast<uint4*>(row_ptr<bf16>(a.O, w.b, w.h, row) + c * 32);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) o4[q] = make_uint4(0, 0, 0, 0);
+                    }
                 }
+            }
+            if (w.T > 0) {
+                if (!parts) store_staged<D>(maps.o, stage, r - lane, w.b, w.h, row - lane, row - lane < a.Nq, lane);
+                if (lane == 0) {   // (nothing staged: at once)
+                    tc::bulk_wait_read();
+                    tc::mbar_arrive(tc::smem_u32(&sh.q_free[(n - 1) & 1]));
+                }
+                __syncwarp();
             }
             if (write) {
                 const float lse = sum == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(sum));
@@ -444,7 +458,8 @@ int launch(const CrossArgs& a, const Plan& plan, float* o_part, float* lse_part,
     const void* fn = (const void*)cross_fwd_sm100_kernel<D>;
     Maps maps;
     const bool pieces = a.k_len != nullptr;
-    if (!make_tile_map(&maps.q, a.Q, a.B, a.Hq, a.Nq, D, BM) ||
+    if (!make_tile_map(&maps.q, a.Q, a.B, a.Hq, a.Nq, D) ||
+        !make_tile_map(&maps.o, a.O, a.B, a.Hq, a.Nq, D, 32) ||
         !make_row_maps(&maps.k, a.K, a.B, a.Hkv, a.Nk, D, pieces) ||
         !make_row_maps(&maps.v, a.V, a.B, a.Hkv, a.Nk, D, pieces))
         return SVGEAR_ERR_CUDA;

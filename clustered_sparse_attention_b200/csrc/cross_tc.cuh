@@ -99,37 +99,33 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Stores 32 bf16 columns of the warp's 32 rows, one row per lane in packed pairs
-// (pk), first row `row0` of `rows`, at base + row * stride (elements).  The four
-// lanes of a quad transpose their 16-byte pieces, so that a store instruction
-// writes 64 contiguous bytes of eight rows instead of 16 bytes of 32.
-__device__ __forceinline__ void store_rows32(__nv_bfloat16* base, int64_t stride, int rows, int lane,
-                                             uint32_t (&pk)[16]) {
+// Output rows leave through a 128-row tile buffer in shared memory (the layout of
+// load_tile) and TMA stores, so that whole lines reach L2: a lane that stores its
+// own row touches 32 lines per instruction, and transposing in registers first
+// measured twice the time.
+// 32 bf16 columns [col, col + 32) of this thread's row, packed in pairs.
+__device__ __forceinline__ void stage_row32(uint32_t tile, int row, int col, const uint32_t (&pk)[16]) {
+    const uint32_t line = tile + (col >> 6) * 16384 + row * 128;
+    const int c0 = (col & 63) >> 3;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        // words w of pieces (0, 1) and (2, 3) change places with lane ^ 2, then of
-        // (0, 2) and (1, 3) with lane ^ 1
-        const bool up2 = lane & 2, up1 = lane & 1;
+    for (int q = 0; q < 4; ++q)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + (((c0 + q) ^ (row & 7)) << 4)),
+                     "r"(pk[4 * q]), "r"(pk[4 * q + 1]), "r"(pk[4 * q + 2]), "r"(pk[4 * q + 3])
+                     : "memory");
+}
+// The warp's 32 staged rows [r0, r0 + 32) of the tile to rows n0.. of head
+// (b, h); rows past the tensor are left out (`map` has boxes of 32 rows).
+template <int D>
+__device__ __forceinline__ void store_staged(const TileMap& map, uint32_t tile, int r0, int b, int h, int n0,
+                                             bool any_row, int lane) {
+    tc::fence_async_smem();
+    __syncwarp();
+    if (lane == 0 && any_row) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            uint32_t &x = pk[4 * j + w], &y = pk[4 * (j + 2) + w];
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, up2 ? x : y, 2);
-            if (up2) x = got; else y = got;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-            uint32_t &x = pk[4 * j + w], &y = pk[4 * (j + 1) + w];
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, up1 ? x : y, 1);
-            if (up1) x = got; else y = got;
-        }
+        for (int g = 0; g < D / 64; ++g)
+            tc::tma_store_4d(&map.box, tile + g * 16384 + r0 * 128, g * 64, n0, h * map.hmul, b * map.bmul);
+        tc::bulk_commit();
     }
-    const int r0 = lane & ~3;
-    __nv_bfloat16* dst = base + (lane & 3) * 8;
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-        if (r0 + t < rows)
-            *reinterpret_cast<uint4*>(dst + (r0 + t) * stride) =
-                make_uint4(pk[4 * t], pk[4 * t + 1], pk[4 * t + 2], pk[4 * t + 3]);
 }
 
 // S (128 x 128) = A B^T over D, both K-major tiles in shared memory.
