@@ -56,16 +56,18 @@ __device__ __forceinline__ float hi(uint64_t x) { return __uint_as_float((uint32
 // their rows in a third.  Rows (TMEM lanes) are keys, columns queries:
 //   S^T = K Q^T -> P^T (over S^T) -> dV += P^T dO
 //   dP^T = V dO^T -> dS^T (over dP^T) -> dK += dS^T Q
-// One thread issues dV(i), S(i + 1), dK(i), dP(i + 1) in this order, so that the
-// weights of i + 1 are computed beside dK(i) and dP(i + 1).  (With a thread for
-// either chain the four products ran interleaved, S(i + 1) came as late as
-// dP(i + 1) and the weights had the tensor pipe idle: 4,000 cycles an iteration.)
+// One thread issues dV(i) and S(i + 1), another dK(i) and dP(i + 1) once S(i + 1)
+// is issued, so that S(i + 1) comes first and the weights of i + 1 are computed
+// beside dK(i) and dP(i + 1).  (Without that order the four products ran
+// interleaved and the weights had the tensor pipe idle, 4,000 cycles an
+// iteration; with one thread for all, its barrier tests and commits left the
+// pipe idle, 3,300.)
 // TMEM: S | dP | dV | dK.
 // A copy takes some 2,000 cycles to arrive.  Q(i) is held from S(i) to dK(i), so
 // its ring has three slots where dO's has two: with two of both, S(i + 1) waited
 // for its Q in every iteration (4,300 cycles each against 2,048 of MMA work).
 // ---------------------------------------------------------------------------
-constexpr int kKvThreads = 12 * 32;   // 0-7 weights, 8 TMA, 9 MMA, 11 lse and delta
+constexpr int kKvThreads = 12 * 32;   // 0-7 weights, 8 TMA, 9 and 10 MMA, 11 lse and delta
 
 template <int D>
 constexpr int kv_q_slots() { return D == 128 ? 3 : 4; }
@@ -83,8 +85,9 @@ struct KvShared {
     uint64_t q_full[4], q_empty[4], g_full[4], g_empty[4];
     uint64_t l_full[2], l_empty[2];
     uint64_t s_full, p_full, dp_full, ds_full;
+    uint64_t s_issued;       // S of the next iteration (if any) is on its way
     uint64_t acc_full, acc_free;
-    uint64_t drain;
+    uint64_t drain[2];
     alignas(16) float neg_lse2[2][BM];   // -lse log2 e of a query tile's rows
     alignas(16) float neg_delta[2][BM];
     uint32_t tmem_base;
@@ -138,7 +141,7 @@ cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* 
         }
         for (int s = 0; s < NG; ++s) {
             tc::mbar_init(tc::smem_u32(&sh.g_full[s]), 1);
-            tc::mbar_init(tc::smem_u32(&sh.g_empty[s]), 1);   // dV, which follows dP
+            tc::mbar_init(tc::smem_u32(&sh.g_empty[s]), 2);   // dV and dP
         }
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(tc::smem_u32(&sh.l_full[s]), 1);
@@ -148,9 +151,11 @@ cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* 
         tc::mbar_init(tc::smem_u32(&sh.p_full), 8);
         tc::mbar_init(tc::smem_u32(&sh.dp_full), 1);
         tc::mbar_init(tc::smem_u32(&sh.ds_full), 8);
-        tc::mbar_init(tc::smem_u32(&sh.acc_full), 1);
+        tc::mbar_init(tc::smem_u32(&sh.s_issued), 1);
+        tc::mbar_init(tc::smem_u32(&sh.acc_full), 2);
         tc::mbar_init(tc::smem_u32(&sh.acc_free), 8);
-        tc::mbar_init(tc::smem_u32(&sh.drain), 1);
+        tc::mbar_init(tc::smem_u32(&sh.drain[0]), 1);
+        tc::mbar_init(tc::smem_u32(&sh.drain[1]), 1);
         sh.abort_flag = 0;
         sh.keep_tmem = 0;
         tc::mbar_init_fence();
@@ -238,57 +243,77 @@ cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* 
             }
         }
     } else if (warp == 9 && lane == 0) {
-        // ------------------------------------------------------------ MMA issue
-        Ring qs, gs;   // Q of the next S, dO of the next dP
-        Ring qk, gv;   // Q of the next dK, dO of the next dV
+        // ------------------------------------------------------ MMA: S and dV
+        Ring qr, gr;
         uint32_t n = 0, i = 0;
         bool ok = true;
         auto issue_s = [&]() {
-            mma_dot<D>(tmem, sK, sQ + qs.slot * kTile);
+            mma_dot<D>(tmem, sK, sQ + qr.slot * kTile);
             tc::commit(tc::smem_u32(&sh.s_full));
-            qs.next(NQ);
-        };
-        auto issue_dp = [&]() {
-            mma_dot<D>(tmem + BN, sV, sG + gs.slot * kTile);
-            tc::commit(tc::smem_u32(&sh.dp_full));
-            gs.next(NG);
+            qr.next(NQ);
         };
         while (ok && p.next(a)) {
             ok = poll_bar(&sh.kv_full, n & 1, abort_flag, err, (4 << 16)) &&
-                 poll_bar(&sh.q_full[qs.slot], qs.phase, abort_flag, err, (5 << 16)) &&
-                 poll_bar(&sh.g_full[gs.slot], gs.phase, abort_flag, err, (5 << 16) + 1);
+                 poll_bar(&sh.q_full[qr.slot], qr.phase, abort_flag, err, (5 << 16));
             if (!ok) break;
             tc::fence_after_sync();
             issue_s();
-            issue_dp();
-            // the first sums overwrite the accumulators: the last must be read out
+            // the first sum overwrites dV: the last must be read out
             if (n > 0 && !(ok = poll_bar(&sh.acc_free, (n - 1) & 1, abort_flag, err, (6 << 16)))) break;
             for (int64_t x = p.first; x < p.last; ++x, ++i) {
                 const bool more = x + 1 < p.last;
-                const uint32_t acc = x > p.first ? 1u : 0u;
-                if ((more && !(ok = poll_bar(&sh.q_full[qs.slot], qs.phase, abort_flag, err, (5 << 16)))) ||
+                if (!(ok = poll_bar(&sh.g_full[gr.slot], gr.phase, abort_flag, err, (5 << 16) + 1)) ||
+                    (more && !(ok = poll_bar(&sh.q_full[qr.slot], qr.phase, abort_flag, err, (5 << 16)))) ||
                     !(ok = poll_bar(&sh.p_full, i & 1, abort_flag, err, (7 << 16))))
                     break;
                 tc::fence_after_sync();
-                const uint32_t g = sG + gv.slot * kTile, q = sQ + qk.slot * kTile;
-                mma_rows_2x64<D>(tmem + 2 * BN, tmem, g, acc);
+                mma_rows_2x64<D>(tmem + 2 * BN, tmem, sG + gr.slot * kTile, x > p.first ? 1u : 0u);
                 if (more) issue_s();
-                tc::commit(tc::smem_u32(&sh.g_empty[gv.slot]));   // dV(i), and dP(i) long before
-                gv.next(NG);
-                if ((more && !(ok = poll_bar(&sh.g_full[gs.slot], gs.phase, abort_flag, err, (5 << 16) + 1))) ||
-                    !(ok = poll_bar(&sh.ds_full, i & 1, abort_flag, err, (8 << 16))))
-                    break;
-                tc::fence_after_sync();
-                mma_rows_2x64<D>(tmem + 2 * BN + D, tmem + BN, q, acc);
-                if (more) issue_dp();
-                tc::commit(tc::smem_u32(&sh.q_empty[qk.slot]));
-                qk.next(NQ);
+                tc::mbar_arrive(tc::smem_u32(&sh.s_issued));
+                tc::commit(tc::smem_u32(&sh.g_empty[gr.slot]));
+                gr.next(NG);
             }
             if (!ok) break;
             tc::commit(tc::smem_u32(&sh.acc_full));
             ++n;
         }
-        drain_mma(&sh.drain, &sh.keep_tmem, err, lost, 9 << 16);
+        drain_mma(&sh.drain[0], &sh.keep_tmem, err, lost, 9 << 16);
+    } else if (warp == 10 && lane == 0) {
+        // ----------------------------------------------------- MMA: dP and dK
+        Ring qr, gr;
+        uint32_t n = 0, i = 0;
+        bool ok = true;
+        auto issue_dp = [&]() {
+            mma_dot<D>(tmem + BN, sV, sG + gr.slot * kTile);
+            tc::commit(tc::smem_u32(&sh.dp_full));
+            tc::commit(tc::smem_u32(&sh.g_empty[gr.slot]));
+            gr.next(NG);
+        };
+        while (ok && p.next(a)) {
+            ok = poll_bar(&sh.kv_full, n & 1, abort_flag, err, (4 << 16) + 1) &&
+                 poll_bar(&sh.g_full[gr.slot], gr.phase, abort_flag, err, (5 << 16) + 2);
+            if (!ok) break;
+            tc::fence_after_sync();
+            issue_dp();
+            if (n > 0 && !(ok = poll_bar(&sh.acc_free, (n - 1) & 1, abort_flag, err, (6 << 16) + 1))) break;
+            for (int64_t x = p.first; x < p.last; ++x, ++i) {
+                const bool more = x + 1 < p.last;
+                if ((more && !(ok = poll_bar(&sh.g_full[gr.slot], gr.phase, abort_flag, err, (5 << 16) + 2))) ||
+                    !(ok = poll_bar(&sh.ds_full, i & 1, abort_flag, err, (8 << 16))) ||
+                    !(ok = poll_bar(&sh.s_issued, i & 1, abort_flag, err, (8 << 16) + 1)))
+                    break;
+                tc::fence_after_sync();
+                // (Q(i) is in shared memory since S(i))
+                mma_rows_2x64<D>(tmem + 2 * BN + D, tmem + BN, sQ + qr.slot * kTile, x > p.first ? 1u : 0u);
+                if (more) issue_dp();
+                tc::commit(tc::smem_u32(&sh.q_empty[qr.slot]));
+                qr.next(NQ);
+            }
+            if (!ok) break;
+            tc::commit(tc::smem_u32(&sh.acc_full));
+            ++n;
+        }
+        drain_mma(&sh.drain[1], &sh.keep_tmem, err, lost, (9 << 16) + 1);
     } else if (warp < 8) {
         // -------------------------------------------------------------- weights
         const int h = warp >> 2, r = tid & 127;
