@@ -444,6 +444,10 @@ cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* 
 // 3,400 cycles per tile for 1,536 of MMA work.  (With S in two buffers and dS over S, S(g + 2) came behind
 // dP(g + 1) and dQ(g) and the weights waited for it: 2,800 cycles per tile.)
 // TMEM: S | dP[0] | dP[1] | dQ.
+// The epilogue warps also fetch each item's key count and its rows' lse and delta
+// an item ahead, so that the weights' warps find them in shared memory.  (With
+// delta = do.o computed there too, from O and dO, they were the slowest warps:
+// 1,540 us for 75,600 x 512 keys against 1,160 and a delta pass of 255.)
 // ---------------------------------------------------------------------------
 constexpr int kQThreads = 16 * 32;   // 0-7 weights, 8 TMA, 9-11 MMA, 12-15 epilogue
 
@@ -454,7 +458,7 @@ constexpr int q_k_slots() { return D == 128 ? 3 : 4; }
 template <int D>
 constexpr int q_v_slots() { return D == 128 ? 2 : 4; }
 template <int D>
-constexpr uint32_t q_smem() { return (2 + q_k_slots<D>() + q_v_slots<D>()) * (D / 64) * 16384 + 1024; }
+constexpr uint32_t q_smem() { return (2 + q_k_slots<D>() + q_v_slots<D>()) * (D / 64) * 16384; }
 
 struct QMaps {
     RowMaps k, v;
@@ -467,7 +471,10 @@ struct QShared {
     uint64_t s_full, s_read;
     uint64_t dp_full[2], ds_full[2], dq_done[2];
     uint64_t acc_full, acc_free;
+    uint64_t row_full[2], row_free[2];   // the item's rows below, in turn
     uint64_t drain[3];
+    float neg_lse2[2][BM], neg_delta[2][BM];
+    int keys[2];
     uint32_t tmem_base;
     int abort_flag;
     int keep_tmem;
@@ -518,7 +525,7 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ QShared sh;
-    const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t base = tc::smem_u32(smem_raw);   // 1024-byte aligned: see launch_dq()
     const uint32_t sQ = base, sG = sQ + kTile, sK = sG + kTile, sV = sK + NK * kTile;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -530,6 +537,10 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
         tc::mbar_init(tc::smem_u32(&sh.ds_full[0]), 8);
         tc::mbar_init(tc::smem_u32(&sh.ds_full[1]), 8);
         tc::mbar_init(tc::smem_u32(&sh.acc_free), 4);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(tc::smem_u32(&sh.row_full[i]), 4);
+            tc::mbar_init(tc::smem_u32(&sh.row_free[i]), 8);
+        }
         for (int i = 0; i < 4; ++i) {
             tc::mbar_init(tc::smem_u32(&sh.k_full[i]), 1);
             tc::mbar_init(tc::smem_u32(&sh.k_empty[i]), 1);
@@ -562,30 +573,36 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
             if (n > 0 && !(ok = poll_bar(&sh.q_empty, (n - 1) & 1, abort_flag, err, (1 << 16)))) break;
             load_tile<D>(maps.q, sQ, w.b, w.h, w.qt * BM, tc::smem_u32(&sh.q_full));
             q_loaded = true;
-            for (int j = 0; j < w.T; ++j) {
+            auto load_k = [&](int j) {
                 if (kfills >= NK && !(ok = poll_bar(&sh.k_empty[kr.slot], kr.phase ^ 1, abort_flag, err, (2 << 16))))
-                    break;
+                    return;
                 load_key_tile<D>(maps.k, sK + kr.slot * kTile, w.b, w.hk, j * BN, w.keys, a.Nk,
                                  tc::smem_u32(&sh.k_full[kr.slot]));
                 ++kfills;
                 kr.next(NK);
-                if (j == 0) {
-                    if (n > 0 && !(ok = poll_bar(&sh.g_empty, (n - 1) & 1, abort_flag, err, (1 << 16) + 1))) break;
-                    load_tile<D>(maps.g, sG, w.b, w.h, w.qt * BM, tc::smem_u32(&sh.g_full));
-                    g_loaded = true;
-                    // the next item's rows on their way from HBM to L2
-                    QItem x = w;
-                    if (x.next(a) && x.T > 0) {
-                        prefetch_tile<D>(maps.q, x.b, x.h, x.qt * BM);
-                        prefetch_tile<D>(maps.g, x.b, x.h, x.qt * BM);
-                    }
-                }
+            };
+            auto load_v = [&](int j) {
                 if (vfills >= NV && !(ok = poll_bar(&sh.v_empty[vr.slot], vr.phase ^ 1, abort_flag, err, (3 << 16))))
-                    break;
+                    return;
                 load_key_tile<D>(maps.v, sV + vr.slot * kTile, w.b, w.hk, j * BN, w.keys, a.Nk,
                                  tc::smem_u32(&sh.v_full[vr.slot]));
                 ++vfills;
                 vr.next(NV);
+            };
+            load_k(0);
+            if (!ok || (n > 0 && !(ok = poll_bar(&sh.g_empty, (n - 1) & 1, abort_flag, err, (1 << 16) + 1)))) break;
+            load_tile<D>(maps.g, sG, w.b, w.h, w.qt * BM, tc::smem_u32(&sh.g_full));
+            g_loaded = true;
+            // the next item's rows on their way from HBM to L2
+            QItem x = w;
+            if (x.next(a) && x.T > 0) {
+                prefetch_tile<D>(maps.q, x.b, x.h, x.qt * BM);
+                prefetch_tile<D>(maps.g, x.b, x.h, x.qt * BM);
+            }
+            load_v(0);
+            for (int j = 1; ok && j < w.T; ++j) {   // V's slots come free before K's
+                load_v(j);
+                if (ok) load_k(j);
             }
             if (!ok) break;
             ++n;
@@ -660,30 +677,21 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
         const uint32_t tS = lane_base + h * HN;
         const float scale_log2 = a.scale * kLog2e;
         const uint64_t xs2 = pack2(scale_log2, scale_log2);
-        uint32_t g = 0;
-        bool ok = true, more = w.start(a);
-        auto row_of = [&](const QItem& x) { return ((size_t)x.b * a.Hq + x.h) * a.Nq + (size_t)x.qt * BM + r; };
-        // this row's lse and delta, read an item ahead
-        float nl = 0.f, nd = 0.f;
-        if (more && w.qt * BM + r < a.Nq) {
-            nl = __ldg(a.lse + row_of(w));
-            nd = __ldg(a.delta + row_of(w));
-        }
-        for (; ok && more;) {
-            const float neg_lse = -nl * kLog2e, neg_delta = -nd;
-            QItem x = w;
-            const bool more_x = x.next(a);
-            nl = nd = 0.f;
-            if (more_x && x.qt * BM + r < a.Nq) {
-                nl = __ldg(a.lse + row_of(x));
-                nd = __ldg(a.delta + row_of(x));
-            }
+        uint32_t g = 0, m = 0;
+        bool ok = true;
+        const int items = a.B * a.Hq * ((a.Nq + BM - 1) / BM);
+        for (int item = blockIdx.x; ok && item < items; item += gridDim.x, ++m) {
+            if (!(ok = warp_poll_bar(&sh.row_full[m & 1], (m >> 1) & 1, abort_flag, err, (14 << 16)))) break;
+            const float neg_lse = sh.neg_lse2[m & 1][r], neg_delta = sh.neg_delta[m & 1][r];
+            const int keys = sh.keys[m & 1];
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.row_free[m & 1]));
             const uint64_t nl2 = pack2(neg_lse, neg_lse), nd2 = pack2(neg_delta, neg_delta);
-            for (int j = 0; j < w.T; ++j, ++g) {
+            for (int j = 0; j * BN < keys; ++j, ++g) {
                 const uint32_t b = g & 1, tP = tS + BN + b * BN;
                 if (!(ok = warp_poll_bar(&sh.s_full, g & 1, abort_flag, err, (11 << 16)))) break;
                 tc::fence_after_sync();
-                const int valid = w.keys - j * BN - h * HN;
+                const int valid = keys - j * BN - h * HN;
                 if (valid < HN) mask_columns<HN>(tS, valid);   // past the keys: p = 0
                 uint32_t v[HN];
                 tc::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
@@ -718,14 +726,33 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.ds_full[b]));
             }
-            w = x;
-            more = more_x;
         }
     } else if (warp >= 12) {
         // ------------------------------------------------------------- epilogue
         const uint32_t tA = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 3 * BN;
-        uint32_t n = 0;
-        for (bool more = w.start(a); more; more = w.next(a)) {
+        uint32_t n = 0, m = 0;
+        // lse and delta of the warp's 32 rows of item number m, and its keys
+        auto prepare = [&](const QItem& x) {
+            const int s = m & 1, r0 = (warp & 3) * 32, row0 = x.qt * BM + r0;
+            const size_t first = ((size_t)x.b * a.Hq + x.h) * a.Nq + row0;
+            const float l = row0 + lane < a.Nq ? __ldg(a.lse + first + lane) : 0.f;
+            const float d = row0 + lane < a.Nq ? __ldg(a.delta + first + lane) : 0.f;
+            if (m >= 2 && !warp_poll_bar(&sh.row_free[s], ((m >> 1) - 1) & 1, abort_flag, err, (15 << 16)))
+                return false;
+            sh.neg_lse2[s][r0 + lane] = -l * kLog2e;
+            sh.neg_delta[s][r0 + lane] = -d;
+            if (lane == 0) sh.keys[s] = x.keys;   // the same from all four warps
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.row_full[s]));
+            ++m;
+            return true;
+        };
+        bool more = w.start(a);
+        if (more && !prepare(w)) more = false;
+        while (more) {
+            QItem x = w;
+            const bool more_x = x.next(a);
+            if (more_x && !prepare(x)) break;
             const int row = w.qt * BM + (warp & 3) * 32 + lane;
             if (w.T > 0) {
                 if (!warp_poll_bar(&sh.acc_full, n & 1, abort_flag, err, (13 << 16))) break;
@@ -755,6 +782,8 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
             if (row < a.Nq)
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+            w = x;
+            more = more_x;
         }
     }
     __syncwarp();
@@ -786,8 +815,7 @@ int launch_dq(const CrossArgs& a, int* err, int* lost, cudaStream_t st) {
         !make_row_maps(&m.k, a.K, a.B, a.Hkv, a.Nk, D, a.k_len != nullptr) ||
         !make_row_maps(&m.v, a.V, a.B, a.Hkv, a.Nk, D, a.k_len != nullptr))
         return SVGEAR_ERR_CUDA;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)q_smem<D>()) != cudaSuccess)
-        return SVGEAR_ERR_CUDA;
+    if (int s = set_aligned_smem(fn, q_smem<D>())) return s;
     const long long items = (long long)a.B * a.Hq * ceil_div(a.Nq, BM);
     cross_dq_sm100_kernel<D><<<(int)(items < kSms ? items : kSms), kQThreads, q_smem<D>(), st>>>(m, a, err, lost);
     count_launches(1);
