@@ -682,7 +682,7 @@ def svgear_cross_attend(Q, K, V, scale=None, k_len=None, O=None, lse=None, check
         O = _new_like(Q)
     o = _view(O, "O", Q, Q.shape)
     if lse is None:
-        lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device)
+        lse = Q.new_empty((dims.B, dims.Hq, dims.Nq), dtype=torch.float32)
     else:
         _dense(lse, "lse", torch.float32, Q.device, Q.shape[:3])
     ws, n = _cross_workspace(CROSS_FORWARD, dims, Q.device)

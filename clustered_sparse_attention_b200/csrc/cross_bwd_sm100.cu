@@ -800,7 +800,8 @@ int launch_dkv(const CrossArgs& a, float* part, int* err, int* lost, cudaStream_
     if (!make_tile_map(&m.q, a.Q, a.B, a.Hq, a.Nq, D, BM) || !make_tile_map(&m.g, a.dO, a.B, a.Hq, a.Nq, D, BM) ||
         !make_tile_map(&m.k, a.K, a.B, a.Hkv, a.Nk, D, BM) || !make_tile_map(&m.v, a.V, a.B, a.Hkv, a.Nk, D, BM))
         return SVGEAR_ERR_CUDA;
-    if (int s = set_aligned_smem(fn, kv_smem<D>())) return s;
+    static std::atomic<unsigned long long> smem_set{0};
+    if (int s = set_aligned_smem(fn, kv_smem<D>(), smem_set)) return s;
     cross_dkv_sm100_kernel<D><<<kSms, kKvThreads, kv_smem<D>(), st>>>(m, a, part, err, lost);
     count_launches(1);
     SVGEAR_LAUNCH_CHECK();
@@ -815,7 +816,8 @@ int launch_dq(const CrossArgs& a, int* err, int* lost, cudaStream_t st) {
         !make_row_maps(&m.k, a.K, a.B, a.Hkv, a.Nk, D, a.k_len != nullptr) ||
         !make_row_maps(&m.v, a.V, a.B, a.Hkv, a.Nk, D, a.k_len != nullptr))
         return SVGEAR_ERR_CUDA;
-    if (int s = set_aligned_smem(fn, q_smem<D>())) return s;
+    static std::atomic<unsigned long long> smem_set{0};
+    if (int s = set_aligned_smem(fn, q_smem<D>(), smem_set)) return s;
     const long long items = (long long)a.B * a.Hq * ceil_div(a.Nq, BM);
     cross_dq_sm100_kernel<D><<<(int)(items < kSms ? items : kSms), kQThreads, q_smem<D>(), st>>>(m, a, err, lost);
     count_launches(1);

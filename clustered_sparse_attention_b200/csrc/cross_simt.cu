@@ -7,11 +7,14 @@
 // ds_ij = p_ij (do_i.v_j - delta_i), dq_i = scale sum_j ds_ij k_j,
 // dk_j = scale sum_i ds_ij q_i, dv_j = sum_i p_ij do_i.
 //
-// 64 x 64 score tiles, groups of 256 threads in a 16 x 16 grid, 4 x 4 scores and
-// 4 x D/16 outputs a thread: eight (S) or five (P V) shared-memory wavefronts
-// per 32 FMA instructions of a warp, so the FMA pipe is the bound.  Rows of
-// the shared tiles are D + 4 floats (16-byte units an odd number apart), so
-// the 16 column threads read 16 rows without a bank conflict.  The backward
+// 64 x 64 score tiles, groups of 128 threads in an 8 x 16 grid, 8 x 4 scores and
+// 8 x D/16 outputs a thread: 16 shared-memory wavefronts per 128 FMA
+// instructions of a warp (4 x 4 scores a thread need 24, and kept the shared
+// memory pipe 70 % busy with the FMA pipe at 46 %; packed FMA pairs measured no
+// faster).  Rows of the shared tiles
+// are D + 4 floats (16-byte units an odd number apart) and a thread's rows are
+// ty, ty + 8, ..., so that neither the 16 column threads nor the two row threads
+// of a warp meet in a bank.  The backward
 // kernels' four tiles leave room for one CTA per SM; two groups share it, one
 // for the scores and one for do.v (then dV and dK, or the halves of dQ's
 // columns), which hides twice the latency of one group.
@@ -26,8 +29,9 @@ namespace svgear {
 namespace {
 
 constexpr int M = kCrossSimtM, N = kCrossSimtN;
-constexpr int kThreads = 256;
-constexpr int kGradThreads = 512;   // two groups
+constexpr int kThreads = 128;
+constexpr int kGradThreads = 256;   // two groups
+constexpr int R = 8;                // rows of a thread
 
 // Starts the copy of rows [n0, n0 + 64) of head (b, h) to fp32 rows of D + 4,
 // zeros from n_end on (part of the thread's next cp.async group).
@@ -42,23 +46,23 @@ __device__ __forceinline__ void copy_tile(float* s, const svgear_tokens& t, int 
     }
 }
 
-// acc[i][j] = A[4 ty + i] . B[tx + 16 j], j < J (the others 0)
+// acc[i][j] = A[ty + 8 i] . B[tx + 16 j], j < J (the others 0)
 template <int D, int J>
 __device__ __forceinline__ void dot_columns(const float* A, const float* Bm, int ty, int tx,
-                                            float (&acc)[4][4]) {
+                                            float (&acc)[R][4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
 #pragma unroll 4
     for (int k = 0; k < D; k += 4) {
-        float4 a[4], c[J];
+        float4 a[R], c[J];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * (D + 4) + k);
+        for (int i = 0; i < R; ++i) a[i] = *reinterpret_cast<const float4*>(A + (ty + 8 * i) * (D + 4) + k);
 #pragma unroll
         for (int j = 0; j < J; ++j) c[j] = *reinterpret_cast<const float4*>(Bm + (tx + 16 * j) * (D + 4) + k);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 acc[i][j] = fmaf(a[i].x, c[j].x, acc[i][j]);
@@ -71,22 +75,22 @@ __device__ __forceinline__ void dot_columns(const float* A, const float* Bm, int
 // The same for a tile of `valid` keys: one with at most 16 skips the rest.
 template <int D>
 __device__ __forceinline__ void dot_tile(const float* A, const float* Bm, int valid, int ty, int tx,
-                                         float (&acc)[4][4]) {
+                                         float (&acc)[R][4]) {
     if (valid <= 16) dot_columns<D, 1>(A, Bm, ty, tx, acc);
     else dot_columns<D, 4>(A, Bm, ty, tx, acc);
 }
 
-// acc[i][4 c + e] += sum_n W[4 ty + i][n] X[n][64 c + 4 tx + e]; W rows of N + 4,
+// acc[i][4 c + e] += sum_n W[ty + 8 i][n] X[n][64 c + 4 tx + e]; W rows of N + 4,
 // X rows of D + 4, n < valid (weights past it are 0); C columns (a multiple of
 // 64, or 32: then two per thread)
 template <int D, int C = D>
 __device__ __forceinline__ void accumulate(const float* W, const float* X, int valid, int ty, int tx,
-                                           float (&acc)[4][C / 16]) {
+                                           float (&acc)[R][C / 16]) {
 #pragma unroll 2
     for (int n = 0; n < min(N, valid); n += 4) {
-        float4 w[4];
+        float4 w[R];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(W + (4 * ty + i) * (N + 4) + n);
+        for (int i = 0; i < R; ++i) w[i] = *reinterpret_cast<const float4*>(W + (ty + 8 * i) * (N + 4) + n);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const float* row = X + (n + q) * (D + 4);
@@ -106,7 +110,7 @@ __device__ __forceinline__ void accumulate(const float* W, const float* X, int v
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < R; ++i) {
                 const float wi = q == 0 ? w[i].x : q == 1 ? w[i].y : q == 2 ? w[i].z : w[i].w;
 #pragma unroll
                 for (int c = 0; c < C / 16; ++c) acc[i][c] = fmaf(wi, x[c], acc[i][c]);
@@ -115,19 +119,20 @@ __device__ __forceinline__ void accumulate(const float* W, const float* X, int v
     }
 }
 
-// acc[i][4 c + e] += sum_q W[q][4 ty + i] X[q][64 c + 4 tx + e] (W transposed)
+// acc[i][4 c + e] += sum_q W[q][8 ty + i] X[q][64 c + 4 tx + e] (W transposed)
 template <int D>
 __device__ __forceinline__ void accumulate_t(const float* W, const float* X, int ty, int tx,
-                                             float (&acc)[4][D / 16]) {
+                                             float (&acc)[R][D / 16]) {
 #pragma unroll 4
     for (int q = 0; q < M; ++q) {
-        const float4 w = *reinterpret_cast<const float4*>(W + q * (N + 4) + 4 * ty);
-        const float wi[4] = {w.x, w.y, w.z, w.w};
+        const float4 w = *reinterpret_cast<const float4*>(W + q * (N + 4) + 8 * ty);
+        const float4 y = *reinterpret_cast<const float4*>(W + q * (N + 4) + 8 * ty + 4);
+        const float wi[R] = {w.x, w.y, w.z, w.w, y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
             const float4 x = *reinterpret_cast<const float4*>(X + q * (D + 4) + 64 * c + 4 * tx);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < R; ++i) {
                 acc[i][4 * c] = fmaf(wi[i], x.x, acc[i][4 * c]);
                 acc[i][4 * c + 1] = fmaf(wi[i], x.y, acc[i][4 * c + 1]);
                 acc[i][4 * c + 2] = fmaf(wi[i], x.z, acc[i][4 * c + 2]);
@@ -173,9 +178,9 @@ cross_fwd_kernel(CrossArgs a, int splits, int tiles_per_split, float* __restrict
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
 
     copy_tile<D>(sQ, a.Q, b, h, q0, a.Nq);
-    float m[4], l[4], o[4][D / 16];
+    float m[R], l[R], o[R][D / 16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
@@ -189,10 +194,10 @@ cross_fwd_kernel(CrossArgs a, int splits, int tiles_per_split, float* __restrict
         tc::cp_async_commit();
         tc::cp_async_wait<1>();
         __syncthreads();
-        float s[4][4];
+        float s[R][4];
         dot_tile<D>(sQ, sK, keys - t * N, ty, tx, s);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < R; ++i) {
             float mx = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -210,7 +215,7 @@ cross_fwd_kernel(CrossArgs a, int splits, int tiles_per_split, float* __restrict
             for (int j = 0; j < 4; ++j) {
                 const float p = expf(s[i][j] - mu);
                 l[i] += p;
-                sP[(4 * ty + i) * (N + 4) + tx + 16 * j] = p;
+                sP[(ty + 8 * i) * (N + 4) + tx + 16 * j] = p;
             }
         }
         tc::cp_async_wait<0>();
@@ -218,9 +223,9 @@ cross_fwd_kernel(CrossArgs a, int splits, int tiles_per_split, float* __restrict
         accumulate<D>(sP, sV, keys - t * N, ty, tx, o);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
         const float sum = row_sum16(l[i]);
-        const int row = q0 + 4 * ty + i;
+        const int row = q0 + ty + 8 * i;
         if (row >= a.Nq) continue;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;   // no key: o = 0, lse = -inf
         const float lse = sum == 0.f ? -INFINITY : m[i] + logf(sum);
@@ -289,24 +294,24 @@ cross_join_kernel(CrossArgs a, int splits, const float* __restrict__ o_part,
 // Backward
 // ---------------------------------------------------------------------------
 // p of one 64 x 64 tile from its scores, into W
-__device__ __forceinline__ void put_weights(const float (&s)[4][4], const float* lse, float* W, int ty, int tx,
+__device__ __forceinline__ void put_weights(const float (&s)[R][4], const float* lse, float* W, int ty, int tx,
                                             int k0, int keys, float scale) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            W[(4 * ty + i) * (N + 4) + tx + 16 * j] =
-                k0 + tx + 16 * j < keys ? expf(s[i][j] * scale - lse[4 * ty + i]) : 0.f;
+            W[(ty + 8 * i) * (N + 4) + tx + 16 * j] =
+                k0 + tx + 16 * j < keys ? expf(s[i][j] * scale - lse[ty + 8 * i]) : 0.f;
 }
 // ds = p (dp - delta) of the same tile, p from W, into G (which may be W)
-__device__ __forceinline__ void put_score_grads(const float (&dp)[4][4], const float* delta, const float* W,
+__device__ __forceinline__ void put_score_grads(const float (&dp)[R][4], const float* delta, const float* W,
                                                 float* G, int ty, int tx) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int x = (4 * ty + i) * (N + 4) + tx + 16 * j;
-            G[x] = W[x] * (dp[i][j] - delta[4 * ty + i]);
+            const int x = (ty + 8 * i) * (N + 4) + tx + 16 * j;
+            G[x] = W[x] * (dp[i][j] - delta[ty + 8 * i]);
         }
 }
 
@@ -321,7 +326,7 @@ __global__ void __launch_bounds__(kGradThreads) cross_dq_kernel(CrossArgs a) {
     __shared__ float s_lse[M], s_delta[M];
     const int b = blockIdx.y / a.Hq, h = blockIdx.y - b * a.Hq, hk = h / a.G;
     const int q0 = blockIdx.x * M, keys = cross_keys(a, b);
-    const int grp = threadIdx.x >> 8, ty = (threadIdx.x >> 4) & 15, tx = threadIdx.x & 15;
+    const int grp = threadIdx.x >> 7, ty = (threadIdx.x >> 4) & 7, tx = threadIdx.x & 15;
     copy_tile<D>(sQ, a.Q, b, h, q0, a.Nq);
     copy_tile<D>(sG, a.dO, b, h, q0, a.Nq);
     copy_tile<D>(sKV, a.K, b, hk, 0, keys);
@@ -333,9 +338,9 @@ __global__ void __launch_bounds__(kGradThreads) cross_dq_kernel(CrossArgs a) {
         s_lse[threadIdx.x] = row < a.Nq ? a.lse[r] : INFINITY;   // past the end: p = 0
         s_delta[threadIdx.x] = row < a.Nq ? a.delta[r] : 0.f;
     }
-    float dq[4][C / 16];
+    float dq[R][C / 16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int c = 0; c < C / 16; ++c) dq[i][c] = 0.f;
     for (int t = 0; t * N < keys; ++t) {
@@ -349,7 +354,7 @@ __global__ void __launch_bounds__(kGradThreads) cross_dq_kernel(CrossArgs a) {
             copy_tile<D>(next + N * (D + 4), a.V, b, hk, (t + 1) * N, keys);
         }
         tc::cp_async_commit();
-        float s[4][4];
+        float s[R][4];
         dot_tile<D>(grp ? sG : sQ, grp ? sV : sK, keys - t * N, ty, tx, s);
         if (grp == 0) put_weights(s, s_lse, sS, ty, tx, t * N, keys, a.scale);
         __syncthreads();
@@ -359,8 +364,8 @@ __global__ void __launch_bounds__(kGradThreads) cross_dq_kernel(CrossArgs a) {
     }
     tc::cp_async_wait<0>();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = q0 + 4 * ty + i;
+    for (int i = 0; i < R; ++i) {
+        const int row = q0 + ty + 8 * i;
         if (row >= a.Nq) continue;
         float* dst = row_ptr<float>(a.dQ, b, h, row) + grp * C;
         if constexpr (C == 64)
@@ -381,7 +386,7 @@ __global__ void __launch_bounds__(kGradThreads) cross_dkv_kernel(CrossArgs a, fl
     float* sP = sV + N * (D + 4);
     float* sS = sP + M * (N + 4);
     __shared__ float s_lse[M], s_delta[M];
-    const int grp = threadIdx.x >> 8, ty = (threadIdx.x >> 4) & 15, tx = threadIdx.x & 15;
+    const int grp = threadIdx.x >> 7, ty = (threadIdx.x >> 4) & 7, tx = threadIdx.x & 15;
     const int qtiles = (a.Nq + M - 1) / M;
     const int64_t per = (int64_t)a.G * qtiles;
     const int64_t total = kv_total_units<N>(a) * per;
@@ -402,9 +407,9 @@ __global__ void __launch_bounds__(kGradThreads) cross_dkv_kernel(CrossArgs a, fl
         };
         copy_q(first);
         tc::cp_async_commit();
-        float acc[4][D / 16];   // group 0: dV, group 1: dK
+        float acc[R][D / 16];   // group 0: dV, group 1: dK
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
         for (int64_t x = first; x < last; ++x) {
@@ -424,24 +429,24 @@ __global__ void __launch_bounds__(kGradThreads) cross_dkv_kernel(CrossArgs a, fl
             }
             tc::cp_async_wait<1>();
             __syncthreads();
-            float s[4][4];
+            float s[R][4];
             dot_tile<D>(grp ? sG : sQ, grp ? sV : sK, valid, ty, tx, s);
             if (grp == 0) put_weights(s, s_lse, sP, ty, tx, k.kt * N, k.keys, a.scale);
             __syncthreads();
             if (grp == 0) {
-                if (4 * ty < valid) accumulate_t<D>(sP, sG, ty, tx, acc);   // rows past the keys are not written
+                if (8 * ty < valid) accumulate_t<D>(sP, sG, ty, tx, acc);   // rows past the keys are not written
             } else {
                 put_score_grads(s, s_delta, sP, sS, ty, tx);
-                asm volatile("bar.sync 1, 256;" ::: "memory");   // group 1
-                if (4 * ty < valid) accumulate_t<D>(sS, sQ, ty, tx, acc);
+                asm volatile("bar.sync 1, 128;" ::: "memory");   // group 1
+                if (8 * ty < valid) accumulate_t<D>(sS, sQ, ty, tx, acc);
             }
         }
         const bool whole = first == 0 && last == per;
         float* pk = part + (((size_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * 2 + (1 - grp)) * N * D;
         const float f = grp ? a.scale : 1.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 4 * ty + i, row = k.kt * N + r;
+        for (int i = 0; i < R; ++i) {
+            const int r = 8 * ty + i, row = k.kt * N + r;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
                 const int col = 64 * c + 4 * tx;

@@ -41,7 +41,10 @@ constexpr int HN = BN / 2;                  // keys of a warpgroup per tile
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kP = BN, kO = 2 * BN;    // TMEM columns of P[0] and O_0
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
-constexpr int kMinSplitTiles = 2;           // fewest key tiles of a split
+constexpr int kMinSplitTiles = 4;           // fewest key tiles of a split: with 2, one query
+                                            // over 512 keys took 14.5 us (two launches)
+                                            // against 14.2 and 9 us more on the host; with
+                                            // 8, over 1,024 keys 18.4 against 16.5
 
 // A copy takes some 2,000 cycles to arrive and S(g + 2) follows S(g + 1) by one
 // tile's softmax (1,500): three K slots.  V(g + 2) has two tiles' time.
@@ -463,7 +466,8 @@ int launch(const CrossArgs& a, const Plan& plan, float* o_part, float* lse_part,
         !make_row_maps(&maps.k, a.K, a.B, a.Hkv, a.Nk, D, pieces) ||
         !make_row_maps(&maps.v, a.V, a.B, a.Hkv, a.Nk, D, pieces))
         return SVGEAR_ERR_CUDA;
-    if (int s = set_aligned_smem(fn, smem_bytes<D>())) return s;
+    static std::atomic<unsigned long long> smem_set{0};
+    if (int s = set_aligned_smem(fn, smem_bytes<D>(), smem_set)) return s;
     cross_fwd_sm100_kernel<D><<<plan.items < kSms ? plan.items : kSms, kThreads, smem_bytes<D>(), st>>>(
         maps, a, plan, a.scale * 1.4426950408889634f, o_part, lse_part, err, lost);
     count_launches(1);

@@ -3,8 +3,11 @@
 // past the batch's key count must read as zeros.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "cross.h"
+#include "ctx_cache.h"
 #include "tc_ptx.cuh"
 #include "tc_wait.cuh"
 #include "tma_host.h"
@@ -213,14 +216,20 @@ __device__ __forceinline__ void mask_columns(uint32_t taddr, int valid) {
 
 // Dynamic shared memory of a kernel whose tiles fill it: the 128-byte swizzle
 // needs 1024-byte aligned tiles, and the dynamic part starts after the static
-// one, which is padded to a multiple of that.
-inline int set_aligned_smem(const void* fn, uint32_t bytes) {
+// one, which is padded to a multiple of that.  Done once per function and
+// context (`done`: the id of the last one; the two calls took 2 us of each
+// launch).
+inline int set_aligned_smem(const void* fn, uint32_t bytes, std::atomic<unsigned long long>& done) {
+    unsigned long long ctx = 0;
+    const bool have = SymbolAddressCache::current_id(&ctx);
+    if (have && done.load(std::memory_order_relaxed) == ctx) return SVGEAR_OK;
     cudaFuncAttributes fa;
     if (cudaFuncGetAttributes(&fa, fn) != cudaSuccess) return SVGEAR_ERR_CUDA;
     if (fa.sharedSizeBytes % 1024 != 0) return SVGEAR_ERR_UNSUPPORTED;
-    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess
-               ? SVGEAR_OK
-               : SVGEAR_ERR_CUDA;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
+        return SVGEAR_ERR_CUDA;
+    if (have) done.store(ctx, std::memory_order_relaxed);
+    return SVGEAR_OK;
 }
 
 // A slot ring's position: slot index and the parity of its current use.
