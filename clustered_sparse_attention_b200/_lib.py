@@ -639,12 +639,14 @@ def _new_like(t):
 def _on_device(fn):
     """Runs a call with the device of its first argument as the current one."""
     @functools.wraps(fn)
-    def call(first, *args, **kw):
-        t = first.codes if isinstance(first, Checkpoint) else first
-        if not t.is_cuda or t.device.index == torch.cuda.current_device():
-            return fn(first, *args, **kw)
+    def call(*args, **kw):
+        t = args[0] if args else next(iter(kw.values()), None)
+        t = t.codes if isinstance(t, Checkpoint) else t
+        if (not isinstance(t, torch.Tensor) or not t.is_cuda
+                or t.device.index == torch.cuda.current_device()):
+            return fn(*args, **kw)
         with torch.cuda.device(t.device):
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
     return call
 
 

@@ -294,6 +294,60 @@ def test_two_calls_at_once():
                 assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("dtype", [FP, BF])
+def test_offsets_past_32_bits(dtype):
+    """Rows of k, v, q and o far apart in one buffer: element offsets past 2^31."""
+    row, N, d = 1 << 16, 33000, 64                       # 2.16e9 elements
+    buf = torch.empty(N * row, dtype=dtype, device="cuda")
+    g = torch.Generator().manual_seed(14)
+    far = [buf.as_strided((1, 2, N, d), (0, d, row, 1), 2 * d * i) for i in range(4)]
+    for t in far:
+        t.copy_(torch.randn(1, 2, N, d, generator=g).to(dtype))
+    q, k, v, O = far
+    few = q[:, :, -3:]
+    o1, l1 = _csa().svgear_cross_attend(few, k, v, 0.1)
+    w, wl, tO, tl = co.forward(few, k, v, 0.1)
+    _within(o1, w, tO, "O")
+    _within(l1, wl, tl, "lse")
+    kk, vv = k[:, :, -70:], v[:, :, -70:]
+    lse = _csa().svgear_cross_attend(q, kk, vv, 0.1, O=O)[1]
+    dense = [t.contiguous() for t in (q, kk, vv)]
+    o2, lse2 = _csa().svgear_cross_attend(*dense, 0.1)
+    assert torch.equal(O, o2) and torch.equal(lse, lse2)
+    do = dense[0] * 0.5
+    got = _csa().svgear_cross_attend_backward(do, q, kk, vv, O, lse, 0.1)
+    want = _csa().svgear_cross_attend_backward(do, *dense, o2, lse2, 0.1)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    c = _csa().svgear_checkpoint_save(q)
+    assert torch.equal(c.codes, _csa().svgear_checkpoint_save(dense[0]).codes)
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+def test_many_batches_and_heads(dtype):
+    """More batches than lanes or CTAs, most of them without keys."""
+    B, Hq, Hkv, Nq, Nk, d = 700, 2, 1, 3, 40, 64
+    q, k, v, do = _inputs(15, B, Hq, Hkv, Nq, Nk, d, dtype)
+    lens = [(7 * b) % 41 if b % 3 == 0 else 0 for b in range(B)]
+    O, lse = _check_forward(q, k, v, lens, 0.2)
+    _check_backward(do, q, k, v, O, lse, lens, 0.2)
+
+
+def test_arguments_by_name_and_given_outputs():
+    csa = _csa()
+    q, k, v, do = _inputs(16, 1, 2, 2, 140, 60, 64, BF)
+    want = csa.svgear_cross_attend(q, k, v)
+    lse = torch.full((1, 2, 140), 9.0, device="cuda")
+    O, got = csa.svgear_cross_attend(Q=q, K=k, V=v, lse=lse)
+    assert got is lse and torch.equal(O, want[0]) and torch.equal(lse, want[1])
+    c = csa.svgear_checkpoint_save(X=q)
+    assert torch.equal(csa.svgear_checkpoint_load(c=c), csa.svgear_checkpoint_load(c))
+    a = csa.svgear_cross_attend_backward(dO=do, Q=q, K=k, V=v, O=O, lse=lse)
+    b = csa.svgear_cross_attend_backward(do, q, k, v, O, lse)
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
+
+
 def test_binding_refusals_on_the_gpu():
     csa = _csa()
     q, k, v, do = _inputs(13, 2, 4, 2, 10, 12, 64, BF)
