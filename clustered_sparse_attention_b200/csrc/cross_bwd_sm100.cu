@@ -85,7 +85,11 @@ struct KvShared {
     uint64_t q_full[4], q_empty[4], g_full[4], g_empty[4];
     uint64_t l_full[2], l_empty[2];
     uint64_t s_full, p_full, dp_full, ds_full;
-    uint64_t s_issued;       // S of the next iteration (if any) is on its way
+    // S of the next iteration (if any) is on its way.  In turn: nothing holds the
+    // arriving thread back until i has been seen, and on one barrier the completion
+    // of i + 1 would make i's look open again; i + 2 follows dP(i + 1), which
+    // follows the wait for i.
+    uint64_t s_issued[2];
     uint64_t acc_full, acc_free;
     uint64_t drain[2];
     alignas(16) float neg_lse2[2][BM];   // -lse log2 e of a query tile's rows
@@ -146,12 +150,12 @@ cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* 
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(tc::smem_u32(&sh.l_full[s]), 1);
             tc::mbar_init(tc::smem_u32(&sh.l_empty[s]), 8);
+            tc::mbar_init(tc::smem_u32(&sh.s_issued[s]), 1);
         }
         tc::mbar_init(tc::smem_u32(&sh.s_full), 1);
         tc::mbar_init(tc::smem_u32(&sh.p_full), 8);
         tc::mbar_init(tc::smem_u32(&sh.dp_full), 1);
         tc::mbar_init(tc::smem_u32(&sh.ds_full), 8);
-        tc::mbar_init(tc::smem_u32(&sh.s_issued), 1);
         tc::mbar_init(tc::smem_u32(&sh.acc_full), 2);
         tc::mbar_init(tc::smem_u32(&sh.acc_free), 8);
         tc::mbar_init(tc::smem_u32(&sh.drain[0]), 1);
@@ -269,7 +273,7 @@ cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* 
                 tc::fence_after_sync();
                 mma_rows_2x64<D>(tmem + 2 * BN, tmem, sG + gr.slot * kTile, x > p.first ? 1u : 0u);
                 if (more) issue_s();
-                tc::mbar_arrive(tc::smem_u32(&sh.s_issued));
+                tc::mbar_arrive(tc::smem_u32(&sh.s_issued[i & 1]));
                 tc::commit(tc::smem_u32(&sh.g_empty[gr.slot]));
                 gr.next(NG);
             }
@@ -300,7 +304,7 @@ cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* 
                 const bool more = x + 1 < p.last;
                 if ((more && !(ok = poll_bar(&sh.g_full[gr.slot], gr.phase, abort_flag, err, (5 << 16) + 2))) ||
                     !(ok = poll_bar(&sh.ds_full, i & 1, abort_flag, err, (8 << 16))) ||
-                    !(ok = poll_bar(&sh.s_issued, i & 1, abort_flag, err, (8 << 16) + 1)))
+                    !(ok = poll_bar(&sh.s_issued[i & 1], (i >> 1) & 1, abort_flag, err, (8 << 16) + 1)))
                     break;
                 tc::fence_after_sync();
                 // (Q(i) is in shared memory since S(i))

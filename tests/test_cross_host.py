@@ -2,11 +2,14 @@
 call below reaches the GPU), and of the tests' 64-bit forms against
 differences."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
 
 import cross_oracle as co
+import cross_protocol
 
 
 @pytest.fixture(scope="module")
@@ -165,3 +168,16 @@ def test_oracle_pack_rule():
     assert exps[0, 0, :, 0].tolist() == [121, 122, 121, 0, 255, 248, 248]
     assert codes[0, 0, :, 0].tolist() == [64, 64, 127, 0, 0, 113, -127]
     assert torch.isnan(co.unpack(codes, exps)[0, 0, 4]).all()
+
+
+@pytest.mark.parametrize("iterations", [1, 2, 3, 7])
+def test_dkv_barriers_never_lap(iterations):
+    """However its roles are delayed, the dK/dV kernel's waits end: a wait that a second
+    completion could overtake would look open again and run into its time limit."""
+    src = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       "clustered_sparse_attention_b200", "csrc", "cross_bwd_sm100.cu")
+    with open(src) as f:
+        m = re.search(r"uint64_t s_issued(\[(\d+)\])?;", f.read())
+    assert cross_protocol.stuck_states(iterations, int(m.group(2) or 1)) == []
+    if iterations > 1:
+        assert cross_protocol.stuck_states(iterations, 1)   # the model sees the fault
