@@ -488,7 +488,7 @@ cross_dkv_join_kernel(CrossArgs a, int qrows, int ctas, const float* __restrict_
             before *= a.Hkv;
         }
         const int64_t total = kv_total_units<BN>(a) * per;
-        if (threadIdx.x == 0) {
+        if (threadIdx.x < 2) {
             // the CTAs whose ranges hold the unit's first and last iteration
             const int64_t s = (before + (int64_t)h * nt + kt) * per, e = s + per - 1;
             auto holder = [&](int64_t it) {
@@ -497,50 +497,53 @@ cross_dkv_join_kernel(CrossArgs a, int qrows, int ctas, const float* __restrict_
                 while (c + 1 < ctas && kv_range(total, c + 1, ctas) <= it) ++c;
                 return c;
             };
-            s_first = holder(s);
-            s_last = holder(e);
-            s_empties = total < ctas;
+            const int c = holder(threadIdx.x == 0 ? s : e);
+            if (threadIdx.x == 0) {
+                s_first = c;
+                s_empties = total < ctas;
+            } else {
+                s_last = c;
+            }
         }
     }
     __syncthreads();
     const bool direct = kt < nt && s_first == s_last;   // written by its CTA
     if (direct && row0 + rows <= keys) return;
-    const int64_t total = direct || kt >= nt || !s_empties ? 0 : kv_total_units<BN>(a) * a.G * ((a.Nq + qrows - 1) / qrows);
-    for (int i = threadIdx.x; i < 2 * rows * (D / 4); i += 256) {
-        const int which = i / (rows * (D / 4)), rem = i - which * rows * (D / 4);
-        const int r = rem / (D / 4), col = (rem - r * (D / 4)) * 4, row = row0 + r;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (row < keys) {
-            if (direct) continue;
-            const float* src = part + (size_t)(row - kt * BN) * D + col + (size_t)which * BN * D;
-            for (int c = s_first; c <= s_last; ++c) {
-                if (s_empties && kv_range(total, c, ctas) == kv_range(total, c + 1, ctas)) continue;
-                const float4 x =
-                    *reinterpret_cast<const float4*>(src + ((size_t)c * 2 + (c == s_first ? 1 : 0)) * 2 * BN * D);
-                v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    // a thread's sums side by side, so that a part's loads are in flight together
+    constexpr int CH = D / 4, V = 2 * kJoinRows * CH / 256;
+    const float* src[V];
+    float4 v[V];
+#pragma unroll
+    for (int x = 0; x < V; ++x) {
+        const int i = threadIdx.x + 256 * x, r = i / CH % kJoinRows, col = i % CH * 4;
+        src[x] = part + ((size_t)(i / (kJoinRows * CH)) * BN + row0 - kt * BN + r) * D + col;
+        v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (!direct && kt < nt) {
+        const int64_t total = s_empties ? kv_total_units<BN>(a) * a.G * ((a.Nq + qrows - 1) / qrows) : 0;
+        for (int c = s_first; c <= s_last; ++c) {
+            if (s_empties && kv_range(total, c, ctas) == kv_range(total, c + 1, ctas)) continue;
+            const size_t at = ((size_t)c * 2 + (c == s_first ? 1 : 0)) * 2 * BN * D;
+            float4 p[V];
+#pragma unroll
+            for (int x = 0; x < V; ++x) p[x] = *reinterpret_cast<const float4*>(src[x] + at);
+#pragma unroll
+            for (int x = 0; x < V; ++x) {
+                v[x].x += p[x].x; v[x].y += p[x].y; v[x].z += p[x].z; v[x].w += p[x].w;
             }
         }
-        store4(row_ptr<T>(which ? a.dV : a.dK, b, h, row) + col, v);
+    }
+#pragma unroll
+    for (int x = 0; x < V; ++x) {
+        const int i = threadIdx.x + 256 * x, row = row0 + i / CH % kJoinRows;
+        if (row >= a.Nk || (direct && row < keys)) continue;
+        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);   // (parts hold anything past the keys)
+        store4(row_ptr<T>(i / (kJoinRows * CH) ? a.dV : a.dK, b, h, row) + i % CH * 4, row < keys ? v[x] : z);
     }
 }
 
-// delta_i = do_i . o_i in fp32, 16 bytes of the row per lane; o from its tensor
-// or from 8-bit codes, and with codes also q unpacked into qx [B][Hq][Nq][D].
-template <typename T>
-__device__ __forceinline__ void held_chunk(const HeldTokens& t, int64_t i, float* x) {
-    constexpr int C = Elem<T>::kPerChunk;
-    const float step = held_step(__ldg(t.exps + i / 32));
-    uint32_t w[C / 4];
-    if constexpr (C == 8) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(t.codes + i));
-        w[0] = v.x;
-        w[1] = v.y;
-    } else {
-        w[0] = __ldg(reinterpret_cast<const uint32_t*>(t.codes + i));
-    }
-#pragma unroll
-    for (int e = 0; e < C; ++e) x[e] = (float)(int8_t)(w[e / 4] >> (8 * (e % 4))) * step;
-}
+constexpr int kHeldUnits = 2;   // units of cross_delta_held_kernel per thread, 256 apart
+
 __device__ __forceinline__ void store_chunk(float* p, const float* x) {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
 }
@@ -554,9 +557,9 @@ __device__ __forceinline__ void store_chunk(__nv_bfloat16* p, const float* x) {
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <typename T, int D, bool HELD>
-__global__ void __launch_bounds__(256)
-cross_delta_kernel(CrossArgs a, HeldTokens qh, HeldTokens oh, T* __restrict__ qx) {
+// delta_i = do_i . o_i in fp32, 16 bytes of the row per lane.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) cross_delta_kernel(CrossArgs a) {
     constexpr int C = Elem<T>::kPerChunk, LR = D / C;   // lanes per row: 8, 16 or 32
     const uint32_t rows = (uint32_t)((int64_t)a.B * a.Hq * a.Nq);
     const uint64_t r64 = ((uint64_t)blockIdx.x * 256 + threadIdx.x) / LR;
@@ -567,21 +570,65 @@ cross_delta_kernel(CrossArgs a, HeldTokens qh, HeldTokens oh, T* __restrict__ qx
     const int b = (int)(bh / (uint32_t)a.Hq), h = (int)(bh - (uint32_t)b * (uint32_t)a.Hq);
     float g[C], o[C];
     Elem<T>::load(row_ptr<const T>(a.dO, b, h, n) + c, g);
-    if (HELD) {
-        const int64_t i = (int64_t)r * D + c;
-        held_chunk<T>(oh, i, o);
-        float q[C];
-        held_chunk<T>(qh, i, q);
-        if (in) store_chunk(qx + i, q);
-    } else {
-        Elem<T>::load(row_ptr<const T>(a.O, b, h, n) + c, o);
-    }
+    Elem<T>::load(row_ptr<const T>(a.O, b, h, n) + c, o);
     float s = 0.f;
 #pragma unroll
     for (int e = 0; e < C; ++e) s = fmaf(g[e], o[e], s);
 #pragma unroll
     for (int x = LR / 2; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
     if (in && c == 0) a.delta[r] = s;
+}
+
+// The same with o from its 8-bit codes, and q unpacked from its own into qx
+// [B][Hq][Nq][D]: 16 elements per lane and unit (16 bytes of codes), the loads of a
+// thread's units up front.
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+cross_delta_held_kernel(CrossArgs a, HeldTokens qh, HeldTokens oh, T* __restrict__ qx) {
+    constexpr int P = 16, LR = D / P, U = kHeldUnits, C = Elem<T>::kPerChunk;
+    const uint32_t rows = (uint32_t)((int64_t)a.B * a.Hq * a.Nq);
+    const uint64_t i0 = (uint64_t)blockIdx.x * (256 * U) + threadIdx.x;
+    const int c = (int)(i0 % LR) * P;
+    uint4 g[U][P / C], oc[U], qc[U];
+    uint32_t oe[U], qe[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint64_t r64 = (i0 + 256 * u) / LR;
+        const uint32_t r = r64 < rows ? (uint32_t)r64 : rows - 1;
+        const uint32_t bh = r / (uint32_t)a.Nq, n = r - bh * (uint32_t)a.Nq;
+        const int b = (int)(bh / (uint32_t)a.Hq), h = (int)(bh - (uint32_t)b * (uint32_t)a.Hq);
+        const T* src = row_ptr<const T>(a.dO, b, h, n) + c;
+        const size_t i = (size_t)r * D + c;
+        oc[u] = __ldg(reinterpret_cast<const uint4*>(oh.codes + i));
+        qc[u] = __ldg(reinterpret_cast<const uint4*>(qh.codes + i));
+        oe[u] = __ldg(oh.exps + i / 32);
+        qe[u] = __ldg(qh.exps + i / 32);
+#pragma unroll
+        for (int k = 0; k < P / C; ++k) g[u][k] = Elem<T>::load_raw(src + k * C);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint64_t r64 = (i0 + 256 * u) / LR;
+        const float ostep = held_step(oe[u]), qstep = held_step(qe[u]);
+        const uint32_t ow[4] = {oc[u].x, oc[u].y, oc[u].z, oc[u].w};
+        const uint32_t qw[4] = {qc[u].x, qc[u].y, qc[u].z, qc[u].w};
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < P / C; ++k) {
+            float x[C], q[C];
+            Elem<T>::unpack(g[u][k], x);
+#pragma unroll
+            for (int e = 0; e < C; ++e) {
+                const int y = k * C + e;
+                s = fmaf(x[e], (float)(int8_t)(ow[y / 4] >> (8 * (y % 4))) * ostep, s);
+                q[e] = (float)(int8_t)(qw[y / 4] >> (8 * (y % 4))) * qstep;
+            }
+            if (r64 < rows) store_chunk(qx + r64 * D + c + k * C, q);
+        }
+#pragma unroll
+        for (int x = LR / 2; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+        if (r64 < rows && c == 0) a.delta[r64] = s;
+    }
 }
 
 template <typename F>
@@ -612,11 +659,12 @@ int join(const CrossArgs& a, int splits, const float* o_part, const float* lse_p
 }
 template <typename T, int D>
 int delta(const CrossArgs& a, const HeldTokens* q, const HeldTokens* o, void* qx, cudaStream_t st) {
-    const int grid = ceil_div((long long)a.B * a.Hq * a.Nq * (D / Elem<T>::kPerChunk), 256);
+    const long long rows = (long long)a.B * a.Hq * a.Nq;
     if (q)
-        cross_delta_kernel<T, D, true><<<grid, 256, 0, st>>>(a, *q, *o, static_cast<T*>(qx));
+        cross_delta_held_kernel<T, D><<<ceil_div(rows * (D / 16), 256 * kHeldUnits), 256, 0, st>>>(
+            a, *q, *o, static_cast<T*>(qx));
     else
-        cross_delta_kernel<T, D, false><<<grid, 256, 0, st>>>(a, HeldTokens{}, HeldTokens{}, nullptr);
+        cross_delta_kernel<T, D><<<ceil_div(rows * (D / Elem<T>::kPerChunk), 256), 256, 0, st>>>(a);
     count_launches(1);
     SVGEAR_LAUNCH_CHECK();
     return SVGEAR_OK;
