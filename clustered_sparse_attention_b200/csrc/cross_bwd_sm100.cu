@@ -758,34 +758,32 @@ cross_dq_sm100_kernel(const __grid_constant__ QMaps maps, CrossArgs a, int* __re
             const bool more_x = x.next(a);
             if (more_x && !prepare(x)) break;
             const int row = w.qt * BM + (warp & 3) * 32 + lane;
-            if (w.T > 0) {
+            if (w.T == 0) {   // no key
+                zero_rows32<D>(a.dQ, w.b, w.h, row - lane, a.Nq, lane);
+            } else {
                 if (!warp_poll_bar(&sh.acc_full, n & 1, abort_flag, err, (13 << 16))) break;
                 tc::fence_after_sync();
                 ++n;
-            }
-            uint4* dst = reinterpret_cast<uint4*>(row_ptr<bf16>(a.dQ, w.b, w.h, row));
-            uint32_t pk[D / 2];
+                uint32_t pk[D / 2];
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                if (w.T > 0) {
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
                     tc::tmem_ld32(tA + c * 32, o);
                     tc::tmem_ld_wait();
-                }
 #pragma unroll
-                for (int e = 0; e < 16; ++e)   // (no key: zeros)
-                    pk[c * 16 + e] = w.T > 0 ? bf16_pair(__uint_as_float(o[2 * e]) * a.scale,
-                                                         __uint_as_float(o[2 * e + 1]) * a.scale)
-                                             : 0u;
-            }
-            if (w.T > 0) {   // the accumulator has been read
-                tc::fence_before_sync();
+                    for (int e = 0; e < 16; ++e)
+                        pk[c * 16 + e] = bf16_pair(__uint_as_float(o[2 * e]) * a.scale,
+                                                   __uint_as_float(o[2 * e + 1]) * a.scale);
+                }
+                tc::fence_before_sync();   // the accumulator has been read
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.acc_free));
-            }
-            if (row < a.Nq)
+                uint4* dst = reinterpret_cast<uint4*>(row_ptr<bf16>(a.dQ, w.b, w.h, row));
+                if (row < a.Nq)
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                    for (int c = 0; c < D / 8; ++c)
+                        dst[c] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+            }
             w = x;
             more = more_x;
         }

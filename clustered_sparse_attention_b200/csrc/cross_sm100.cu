@@ -357,52 +357,45 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
             const bool write = row < a.Nq;
             const size_t rr = ((size_t)w.b * a.Hq + w.h) * a.Nq + row;
             const size_t part = (size_t)w.split * a.B * a.Hq * a.Nq + rr;
-            float sum = 0.f, m = 0.f, c0 = 0.f, c1 = 0.f;
-            if (w.T > 0) {
-                if (!warp_poll_bar(&sh.ml_full, n & 1, abort_flag, err, (13 << 16))) break;
-                const float2 x0 = sh.ml[0][r], x1 = sh.ml[1][r];
-                m = fmaxf(x0.x, x1.x);
-                const float mu = m == -INFINITY ? 0.f : m;   // no finite score
-                c0 = tc::ex2(x0.x - mu);
-                c1 = tc::ex2(x1.x - mu);
-                sum = fmaf(c0, x0.y, c1 * x1.y);
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                c0 *= inv;
-                c1 *= inv;
-                if (!warp_poll_bar(&sh.o_full, n & 1, abort_flag, err, (15 << 16))) break;
-                tc::fence_after_sync();
-                ++n;
+            if (w.T == 0) {   // no key
+                if (!parts) zero_rows32<D>(a.O, w.b, w.h, row - lane, a.Nq, lane);
+                if (write) (parts ? lse_part[part] : a.lse[rr]) = -INFINITY;
+                continue;
             }
+            if (!warp_poll_bar(&sh.ml_full, n & 1, abort_flag, err, (13 << 16))) break;
+            const float2 x0 = sh.ml[0][r], x1 = sh.ml[1][r];
+            const float m = fmaxf(x0.x, x1.x);
+            const float mu = m == -INFINITY ? 0.f : m;   // no finite score
+            float c0 = tc::ex2(x0.x - mu), c1 = tc::ex2(x1.x - mu);
+            const float sum = fmaf(c0, x0.y, c1 * x1.y);
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            c0 *= inv;
+            c1 *= inv;
+            if (!warp_poll_bar(&sh.o_full, n & 1, abort_flag, err, (15 << 16))) break;
+            tc::fence_after_sync();
             // 32 columns of both accumulators at a time (beside running MMAs a
             // TMEM load takes some 350 cycles whatever its size) in a rolled
             // loop (this code runs once per item, fetched anew each time)
-            const uint32_t stage = sQ + ((n - 1) & 1) * kTile;
+            const uint32_t stage = sQ + (n & 1) * kTile;
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o0[32], o1[32];
-                if (w.T > 0) {
-                    tc::tmem_ld32(tO + c * 32, o0);
-                    tc::tmem_ld32(tO + D + c * 32, o1);
-                    tc::tmem_ld_wait();
-                    if (c == D / 32 - 1) {   // the accumulators and the pair have been read
-                        tc::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.o_free));
-                    }
+                tc::tmem_ld32(tO + c * 32, o0);
+                tc::tmem_ld32(tO + D + c * 32, o1);
+                tc::tmem_ld_wait();
+                if (c == D / 32 - 1) {   // the accumulators and the pair have been read
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.o_free));
                 }
-                if (w.T > 0) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        uint32_t y0, y1;
-                        fma2(o1[e], o1[e + 1], pack2(c1, c1), 0ull, y0, y1);
-                        fma2(o0[e], o0[e + 1], pack2(c0, c0), (uint64_t)y0 | ((uint64_t)y1 << 32), o0[e], o0[e + 1]);
-                    }
-                } else {   // no key
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o0[e] = 0;
+                for (int e = 0; e < 32; e += 2) {
+                    uint32_t y0, y1;
+                    fma2(o1[e], o1[e + 1], pack2(c1, c1), 0ull, y0, y1);
+                    fma2(o0[e], o0[e + 1], pack2(c0, c0), (uint64_t)y0 | ((uint64_t)y1 << 32), o0[e], o0[e + 1]);
                 }
                 if (parts) {
-                    if (write && w.T > 0) {
+                    if (write) {
                         uint4* o4 = reinterpret_cast<uint4*>(o_part + part * D + c * 32);
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
@@ -413,23 +406,16 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         pk[e] = bf16_pair(__uint_as_float(o0[2 * e]), __uint_as_float(o0[2 * e + 1]));
-                    if (w.T > 0) {
-                        stage_row32(stage, r, c * 32, pk);
-                    } else if (write) {
-                        uint4* o4 = reinterpret_cast<uint4*>(row_ptr<bf16>(a.O, w.b, w.h, row) + c * 32);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) o4[q] = make_uint4(0, 0, 0, 0);
-                    }
+                    stage_row32(stage, r, c * 32, pk);
                 }
             }
-            if (w.T > 0) {
-                if (!parts) store_staged<D>(maps.o, stage, r - lane, w.b, w.h, row - lane, row - lane < a.Nq, lane);
-                if (lane == 0) {   // (nothing staged: at once)
-                    tc::bulk_wait_read();
-                    tc::mbar_arrive(tc::smem_u32(&sh.q_free[(n - 1) & 1]));
-                }
-                __syncwarp();
+            if (!parts) store_staged<D>(maps.o, stage, r - lane, w.b, w.h, row - lane, row - lane < a.Nq, lane);
+            if (lane == 0) {   // (nothing staged: at once)
+                tc::bulk_wait_read();
+                tc::mbar_arrive(tc::smem_u32(&sh.q_free[n & 1]));
             }
+            __syncwarp();
+            ++n;
             if (write) {
                 const float lse = sum == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(sum));
                 if (parts) lse_part[part] = lse;

@@ -131,6 +131,19 @@ __device__ __forceinline__ void store_staged(const TileMap& map, uint32_t tile, 
     }
 }
 
+// Zeros in rows [n0, n0 + 32) of head (b, h) that the tensor has, a warp's lanes
+// along the rows.
+template <int D>
+__device__ __forceinline__ void zero_rows32(const svgear_tokens& t, int b, int h, int n0, int N, int lane) {
+    constexpr int L = D / 8, R = 32 / L;   // lanes per row, rows at a time
+#pragma unroll 4
+    for (int i = 0; i < 32; i += R) {
+        const int row = n0 + i + lane / L;
+        if (row < N)
+            *reinterpret_cast<uint4*>(row_ptr<__nv_bfloat16>(t, b, h, row) + lane % L * 8) = make_uint4(0, 0, 0, 0);
+    }
+}
+
 // S (128 x 128) = A B^T over D, both K-major tiles in shared memory.
 template <int D>
 __device__ __forceinline__ void mma_dot(uint32_t d_tmem, uint32_t sA, uint32_t sB) {
