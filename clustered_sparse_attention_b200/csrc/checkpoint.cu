@@ -7,7 +7,8 @@
 // 1/127 of the group's largest magnitude (2^e where codes saturate).
 //
 // Memory-bound: four units of 16 elements a thread (one 16-byte store of codes
-// each, one exponent byte per two threads).
+// each, one exponent byte per two threads).  75,600 x 40 x 128 bf16 saved and loaded in
+// 381-412 us, 0.87-0.94 of the measured copy rate; 431 us with one unit a thread.
 #include "common.cuh"
 #include "cross.h"
 #include "launchers.h"

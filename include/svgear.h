@@ -404,8 +404,8 @@ int svgear_diagnostics(const void* Qp, const void* Kp, const void* Vp, svgear_di
                        float* recall, float* err2, float* ref2, void* stream);
 
 /* Device status of the last svgear_cluster, svgear_kmeans_assign,
- * svgear_attend or svgear_selftest_wait that used `ws`: writes 4 int32 to
- * status[0..3] (host memory) and synchronises `stream`.  status[0] is 0 when
+ * svgear_attend, svgear_cross_attend(_backward, _backward_ckpt) or
+ * svgear_selftest_wait that used `ws`: writes 4 int32 to status[0..3] (host memory) and synchronises `stream`.  status[0] is 0 when
  * every wait in the tensor-core kernels completed, SVGEAR_ERR_TIMEOUT when a
  * bounded wait gave up (the kernel drained what it had issued and returned;
  * its outputs are not valid), SVGEAR_ERR_TMEM_LOST when a kernel refused to
@@ -418,8 +418,9 @@ int svgear_diagnostics(const void* Qp, const void* Kp, const void* Vp, svgear_di
  * tensor memory, and on that SM no later tensor-core kernel could allocate
  * any.  Every tensor-core kernel checks a device word for this before it
  * allocates and returns SVGEAR_ERR_TMEM_LOST at once; once this call has seen
- * the word set, svgear_cluster and svgear_kmeans_assign on bf16 tokens and
- * svgear_attend(_var) on bf16 return SVGEAR_ERR_TMEM_LOST without launching.
+ * the word set, svgear_cluster, svgear_kmeans_assign,
+ * svgear_attend(_var) and the cross attention calls on bf16 tokens return
+ * SVGEAR_ERR_TMEM_LOST without launching a tensor-core kernel.
  * The state lasts as long as the CUDA context (the process, or until a
  * device reset); nothing clears it.  The library's own extension, with no
  * counterpart in the method. */
