@@ -16,6 +16,8 @@ struct CrossArgs {
     const int32_t* k_len;                       // [B] or NULL
     float* lse;                                 // [B][Hq][Nq]
     float* delta;                               // [B][Hq][Nq] do.o (workspace)
+    float* dq_part;                             // fp32 backward: see cross_dq_part_floats
+    int* status;                                // device status words, where a kernel clears them
     int B, Hq, Hkv, G, Nq, Nk, D;
     float scale;
 };
@@ -93,6 +95,20 @@ __device__ __forceinline__ int64_t kv_range(int64_t total, int c, int ctas) {
 
 // Rows per CTA and keys per tile of the SIMT kernels.
 constexpr int kCrossSimtM = 64, kCrossSimtN = 64;
+// fp32 backward: the dK/dV kernel leaves each key tile's part of dQ ([key tile][B][Hq]
+// [Nq][d]) for a join, so that the scores are computed once for all three gradients (five
+// products instead of seven; gradients of 2,049 x 257 keys, 8 heads, d = 128: 203 us,
+// without 277).  Writing and reading a part costs some 1.6 us of an SM where the two
+// products cost 9, so what limits the parts is their size: at most kCrossDqTiles times
+// dQ, and kCrossDqBytes.  Past that (0) dQ has a kernel of its own.
+constexpr int kCrossDqTiles = 8;
+constexpr long long kCrossDqBytes = 512ll << 20;
+inline size_t cross_dq_part_floats(const svgear_cross_dims& d) {
+    const long long tiles = (d.Nk + (long long)kCrossSimtN - 1) / kCrossSimtN;
+    if (d.dtype != SVGEAR_F32 || tiles > kCrossDqTiles) return 0;
+    const long long n = tiles * d.B * d.Hq * d.Nq * d.d;
+    return n * (long long)sizeof(float) <= kCrossDqBytes ? (size_t)n : 0;
+}
 // Keys per tile of the tensor-core kernels.
 constexpr int kCrossTcN = 128;
 

@@ -118,6 +118,7 @@ struct BwdWs {
     float* delta;   // [B][Hq][Nq]
     char* qx;       // q unpacked from its checkpoint [B][Hq][Nq][d]
     float* part;    // [kSms][2][dK, dV][keys per tile][d] partial sums
+    float* dq_part; // NULL without
 };
 BwdWs carve_bwd(Carve& cv, const svgear_cross_dims& d, bool held) {
     BwdWs w;
@@ -125,6 +126,9 @@ BwdWs carve_bwd(Carve& cv, const svgear_cross_dims& d, bool held) {
     w.delta = cv.take<float>(rows_of(d));
     w.qx = cv.take<char>(held ? rows_of(d) * d.d * (d.dtype == SVGEAR_F32 ? 4 : 2) : 0);
     w.part = cv.take<float>((size_t)kSms * 2 * 2 * (d.dtype == SVGEAR_BF16 ? kCrossTcN : kCrossSimtN) * d.d);
+    const size_t dq = cross_dq_part_floats(d);
+    w.dq_part = cv.take<float>(dq);
+    if (dq == 0) w.dq_part = nullptr;
     return w;
 }
 
@@ -163,7 +167,8 @@ int backward(svgear_tokens dO, svgear_tokens Q, const HeldTokens* qh, svgear_tok
     a.Q = Q; a.K = K; a.V = V; a.O = O; a.dO = dO; a.dQ = dQ; a.dK = dK; a.dV = dV;
     a.lse = const_cast<float*>(lse);
     a.delta = w.delta;
-    if (cudaMemsetAsync(w.status, 0, 4 * sizeof(int), st) != cudaSuccess) return SVGEAR_ERR_CUDA;
+    a.dq_part = w.dq_part;
+    a.status = w.status;   // cleared by the delta kernel
     if ((s = launch_cross_delta(a, dims.dtype, qh, oh, w.qx, st))) return s;
     return dims.dtype == SVGEAR_BF16 ? launch_cross_backward_sm100(a, w.part, w.status, st)
                                      : launch_cross_backward_simt(a, kSms, w.part, st);
@@ -214,9 +219,13 @@ int svgear_cross_attend(svgear_tokens Q, svgear_tokens K, svgear_tokens V, svgea
     CrossArgs a = make_args(dims, k_len, scale);
     a.Q = Q; a.K = K; a.V = V; a.O = O;
     a.lse = lse;
-    if (cudaMemsetAsync(w.status, 0, 4 * sizeof(int), st) != cudaSuccess) return SVGEAR_ERR_CUDA;
-    s = dims.dtype == SVGEAR_BF16 ? launch_cross_sm100(a, w.o_part, w.lse_part, w.status, st)
-                                  : launch_cross_simt(a, w.sp, w.o_part, w.lse_part, st);
+    if (dims.dtype == SVGEAR_BF16) {
+        if (cudaMemsetAsync(w.status, 0, 4 * sizeof(int), st) != cudaSuccess) return SVGEAR_ERR_CUDA;
+        s = launch_cross_sm100(a, w.o_part, w.lse_part, w.status, st);
+    } else {
+        a.status = w.status;
+        s = launch_cross_simt(a, w.sp, w.o_part, w.lse_part, st);
+    }
     if (s) return s;
     return w.parts > 1 ? launch_cross_join(a, dims.dtype, w.parts, w.o_part, w.lse_part, st)
                        : SVGEAR_OK;

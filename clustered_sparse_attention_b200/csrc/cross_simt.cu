@@ -167,6 +167,12 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
     *reinterpret_cast<uint2*>(p) = u;
 }
 
+// The device status words: no kernel of this file waits, so one of them clears the
+// words (a memset of its own costs a small call 2 us).
+__device__ __forceinline__ void clear_status(const CrossArgs& a) {
+    if ((blockIdx.x | blockIdx.y) == 0 && threadIdx.x < 4) a.status[threadIdx.x] = 0;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads)
 cross_fwd_kernel(CrossArgs a, int splits, int tiles_per_split, float* __restrict__ o_part,
@@ -177,6 +183,7 @@ cross_fwd_kernel(CrossArgs a, int splits, int tiles_per_split, float* __restrict
     float* sV = sK + N * (D + 4);
     float* sP = sV + N * (D + 4);
     const int qt = blockIdx.x / splits, sp = blockIdx.x - qt * splits;
+    clear_status(a);
     const int b = blockIdx.y / a.Hq, h = blockIdx.y - b * a.Hq, hk = h / a.G;
     const int q0 = qt * M, keys = cross_keys(a, b);
     const int t0 = sp * tiles_per_split, t1 = min((keys + N - 1) / N, t0 + tiles_per_split);
@@ -320,6 +327,15 @@ __device__ __forceinline__ void put_score_grads(const float (&dp)[R][4], const f
         }
 }
 
+// a thread's columns of a row of C, as accumulate() has them, times f
+template <int C>
+__device__ __forceinline__ void store_half(float* dst, const float (&x)[C / 16], float f, int tx) {
+    if constexpr (C == 64)
+        store4(dst + 4 * tx, make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f));
+    else
+        *reinterpret_cast<float2*>(dst + 2 * tx) = make_float2(x[0] * f, x[1] * f);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kGradThreads) cross_dq_kernel(CrossArgs a) {
     constexpr int C = D / 2;   // dQ columns of a group
@@ -372,16 +388,12 @@ __global__ void __launch_bounds__(kGradThreads) cross_dq_kernel(CrossArgs a) {
     for (int i = 0; i < R; ++i) {
         const int row = q0 + ty + 8 * i;
         if (row >= a.Nq) continue;
-        float* dst = row_ptr<float>(a.dQ, b, h, row) + grp * C;
-        if constexpr (C == 64)
-            store4(dst + 4 * tx, make_float4(dq[i][0] * a.scale, dq[i][1] * a.scale, dq[i][2] * a.scale,
-                                             dq[i][3] * a.scale));
-        else
-            *reinterpret_cast<float2*>(dst + 2 * tx) = make_float2(dq[i][0] * a.scale, dq[i][1] * a.scale);
+        store_half<C>(row_ptr<float>(a.dQ, b, h, row) + grp * C, dq[i], a.scale, tx);
     }
 }
 
-template <int D>
+// DQ: also the key tile's part of dQ, half its columns a group.
+template <int D, bool DQ>
 __global__ void __launch_bounds__(kGradThreads) cross_dkv_kernel(CrossArgs a, float* __restrict__ part) {
     extern __shared__ float sm[];
     float* sQ2 = sm;                               // Q of two tiles
@@ -440,10 +452,27 @@ __global__ void __launch_bounds__(kGradThreads) cross_dkv_kernel(CrossArgs a, fl
             __syncthreads();
             if (grp == 0) {
                 if (8 * ty < valid) accumulate_t<D>(sP, sG, ty, tx, acc);   // rows past the keys are not written
+                if constexpr (DQ) asm volatile("bar.sync 2, 256;" ::: "memory");   // ds from group 1
             } else {
                 put_score_grads(s, s_delta, sP, sS, ty, tx);
                 asm volatile("bar.sync 1, 128;" ::: "memory");   // group 1
+                if constexpr (DQ) asm volatile("bar.arrive 2, 256;" ::: "memory");
                 if (8 * ty < valid) accumulate_t<D>(sS, sQ, ty, tx, acc);
+            }
+            if constexpr (DQ) {
+                constexpr int C = D / 2;
+                float dq[R][C / 16];
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+#pragma unroll
+                    for (int c = 0; c < C / 16; ++c) dq[i][c] = 0.f;
+                accumulate<D, C>(sS, sK + grp * C, valid, ty, tx, dq);
+                float* pq = a.dq_part + (((size_t)k.kt * a.B + k.b) * a.Hq + h) * a.Nq * D + grp * C;
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const int row = q0 + ty + 8 * i;
+                    if (row < a.Nq) store_half<C>(pq + (size_t)row * D, dq[i], 1.f, tx);
+                }
             }
         }
         const bool whole = first == 0 && last == per;
@@ -466,6 +495,29 @@ __global__ void __launch_bounds__(kGradThreads) cross_dkv_kernel(CrossArgs a, fl
         it += last - first;
         tc::cp_async_wait<0>();
     }
+}
+
+// dQ from its key tiles' parts, in their order (none: zeros); 16 bytes a thread.
+template <int D>
+__global__ void __launch_bounds__(256) cross_dq_join_kernel(CrossArgs a) {
+    const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / (D / 4);
+    if (r >= rows) return;
+    const int col = (int)(i % (D / 4)) * 4;
+    const int bh = (int)(r / a.Nq), b = bh / a.Hq, h = bh - b * a.Hq;
+    const int nt = (cross_keys(a, b) + N - 1) / N;
+    float4 p[kCrossDqTiles];   // every load before the first use
+#pragma unroll
+    for (int t = 0; t < kCrossDqTiles; ++t)
+        if (t < nt) p[t] = *reinterpret_cast<const float4*>(a.dq_part + (t * rows + r) * D + col);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int t = 0; t < kCrossDqTiles; ++t)
+        if (t < nt) {
+            v.x += p[t].x; v.y += p[t].y; v.z += p[t].z; v.w += p[t].w;
+        }
+    store4(row_ptr<float>(a.dQ, b, h, r - (int64_t)bh * a.Nq) + col,
+           make_float4(v.x * a.scale, v.y * a.scale, v.z * a.scale, v.w * a.scale));
 }
 
 // Joins the partial sums of units cut between CTAs (in CTA order) and writes
@@ -568,6 +620,7 @@ __device__ __forceinline__ void store_chunk(__nv_bfloat16* p, const float* x) {
 template <typename T, int D>
 __global__ void __launch_bounds__(256) cross_delta_kernel(CrossArgs a) {
     constexpr int C = Elem<T>::kPerChunk, LR = D / C;   // lanes per row: 8, 16 or 32
+    clear_status(a);
     const uint32_t rows = (uint32_t)((int64_t)a.B * a.Hq * a.Nq);
     const uint64_t r64 = ((uint64_t)blockIdx.x * 256 + threadIdx.x) / LR;
     const bool in = r64 < rows;
@@ -594,6 +647,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256)
 cross_delta_held_kernel(CrossArgs a, HeldTokens qh, HeldTokens oh, T* __restrict__ qx) {
     constexpr int P = 16, LR = D / P, U = kHeldUnits, C = Elem<T>::kPerChunk;
+    clear_status(a);
     const uint32_t rows = (uint32_t)((int64_t)a.B * a.Hq * a.Nq);
     const uint64_t i0 = (uint64_t)blockIdx.x * (256 * U) + threadIdx.x;
     const int c = (int)(i0 % LR) * P;
@@ -687,10 +741,18 @@ int dq(const CrossArgs& a, cudaStream_t st) {
     return SVGEAR_OK;
 }
 template <int D>
+int dq_join(const CrossArgs& a, cudaStream_t st) {
+    const long long rows = (long long)a.B * a.Hq * a.Nq;
+    cross_dq_join_kernel<D><<<ceil_div(rows * (D / 4), 256), 256, 0, st>>>(a);
+    count_launches(1);
+    SVGEAR_LAUNCH_CHECK();
+    return SVGEAR_OK;
+}
+template <int D, bool DQ>
 int dkv(const CrossArgs& a, int ctas, float* part, cudaStream_t st) {
     const size_t smem = sizeof(float) * (5 * 64 * (D + 4) + 2 * M * (N + 4));
-    if (int s = set_smem(cross_dkv_kernel<D>, smem)) return s;
-    cross_dkv_kernel<D><<<ctas, kGradThreads, smem, st>>>(a, part);
+    if (int s = set_smem(cross_dkv_kernel<D, DQ>, smem)) return s;
+    cross_dkv_kernel<D, DQ><<<ctas, kGradThreads, smem, st>>>(a, part);
     count_launches(1);
     SVGEAR_LAUNCH_CHECK();
     return SVGEAR_OK;
@@ -729,9 +791,17 @@ int launch_cross_dkv_join(const CrossArgs& a, int dtype, int rows, int ctas, con
     return SVGEAR_PICK(dkv_join, a, rows, ctas, part, st);
 }
 int launch_cross_backward_simt(const CrossArgs& a, int ctas, float* part, cudaStream_t st) {
-    int s = a.D == 128 ? dq<128>(a, st) : dq<64>(a, st);
+    int s;
+    if (a.dq_part) {
+        s = a.D == 128 ? dkv<128, true>(a, ctas, part, st) : dkv<64, true>(a, ctas, part, st);
+        if (s) return s;
+        s = a.D == 128 ? dq_join<128>(a, st) : dq_join<64>(a, st);
+    } else {
+        s = a.D == 128 ? dq<128>(a, st) : dq<64>(a, st);
+        if (s) return s;
+        s = a.D == 128 ? dkv<128, false>(a, ctas, part, st) : dkv<64, false>(a, ctas, part, st);
+    }
     if (s) return s;
-    if ((s = a.D == 128 ? dkv<128>(a, ctas, part, st) : dkv<64>(a, ctas, part, st))) return s;
     return launch_cross_dkv_join(a, SVGEAR_F32, M, ctas, part, st);
 }
 

@@ -114,6 +114,16 @@ def test_many_queries_over_few_keys(dtype):
     _check_backward(do, q, k, v, O, lse, [77, 13], 0.125)
 
 
+@pytest.mark.parametrize("layout", ["head", "token"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nk,lens", [(512, [512, 0, 449]), (513, [513, 0, 512]), (64, [64, 1, 0]), (65, [65, 64, 0])])
+def test_fp32_gradients_either_side_of_the_key_limit(Nk, lens, d, layout):
+    """fp32 dQ comes from the dK/dV kernel's parts up to 512 keys, from its own kernel past that."""
+    q, k, v, do = _inputs(17, 3, 4, 2, 133, Nk, d, FP, layout)
+    O, lse = _check_forward(q, k, v, lens, d ** -0.5)
+    _check_backward(do, q, k, v, O, lse, lens, d ** -0.5)
+
+
 @pytest.mark.parametrize("dtype", [FP, BF])
 @pytest.mark.parametrize("d", [64, 128])
 def test_peaked_scores(dtype, d):
