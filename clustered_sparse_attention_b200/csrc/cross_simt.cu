@@ -20,9 +20,10 @@
 // columns), which hides twice the latency of one group.
 //
 // Bound by issue: with two warps a scheduler the FMA pipe runs at 0.47 (dQ) and 0.51
-// (dK, dV) of its rate and 0.8 of all instructions are FMAs; gradients of 2,049 x 257
-// keys, 8 heads, d = 128: 277 us, of them dQ 125 and dK, dV 152 (seven products, 27
-// TFLOP/s).  A library chain of five products takes 258.
+// (dK, dV) of its rate and 0.8 of all instructions are FMAs.  Gradients of 2,049 x 257
+// keys, 8 heads, d = 128: 203 us with dQ from the dK/dV kernel (27 TFLOP/s; a library
+// chain of the same five products takes 256), 277 with a dQ kernel (see
+// cross_dq_part_floats).
 #include <math.h>
 
 #include "common.cuh"
@@ -497,7 +498,8 @@ __global__ void __launch_bounds__(kGradThreads) cross_dkv_kernel(CrossArgs a, fl
     }
 }
 
-// dQ from its key tiles' parts, in their order (none: zeros); 16 bytes a thread.
+// dQ from its key tiles' parts, in their order (none: zeros); 16 bytes a thread, bound by
+// the parts' bytes (mostly in L2).
 template <int D>
 __global__ void __launch_bounds__(256) cross_dq_join_kernel(CrossArgs a) {
     const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
