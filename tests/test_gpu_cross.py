@@ -460,6 +460,82 @@ def test_backward_from_checkpoints(shape, dtype, d):
     assert got[0].stride() == do.stride()
 
 
+@pytest.mark.parametrize("dtype", [FP, BF])
+def test_checkpoints_captured_and_replayed(dtype):
+    csa = _csa()
+    q, k, v, do = _inputs(41, 2, 4, 2, 201, 140, 128, dtype)
+    kl = _klen([140, 64])
+    O, lse = csa.svgear_cross_attend(q, k, v, k_len=kl)
+
+    def run():
+        qc, oc = csa.svgear_checkpoint_save(q), csa.svgear_checkpoint_save(O)
+        return (csa.svgear_checkpoint_load(qc),) + csa.svgear_cross_attend_backward_ckpt(
+            do, qc, k, v, oc, lse, k_len=kl)
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for gain in (1.0, 0.25):        # new values in the captured buffers
+        do.mul_(gain)
+        q.mul_(gain)
+        want = run()
+        for t in out:
+            t.fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(out, want):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+def test_status_words_of_a_used_workspace_are_cleared(dtype, monkeypatch):
+    csa = _csa()
+    from clustered_sparse_attention_b200 import _lib
+    q, k, v, do = _inputs(42, 1, 2, 2, 40, 70, 64, dtype)
+    plain = _lib._cross_workspace
+
+    def dirty(op, dims, device):
+        ws, n = plain(op, dims, device)
+        return ws.fill_(255), n
+
+    monkeypatch.setattr(_lib, "_cross_workspace", dirty)
+    O, lse = csa.svgear_cross_attend(q, k, v, check_status=True)
+    got = csa.svgear_cross_attend_backward(do, q, k, v, O, lse, check_status=True)
+    c = csa.svgear_checkpoint_save(q), csa.svgear_checkpoint_save(O)
+    held = csa.svgear_cross_attend_backward_ckpt(do, c[0], k, v, c[1], lse, check_status=True)
+    want, tol = co.backward(do, q, k, v, O, lse, 64 ** -0.5, None)
+    for g, w, t, name in zip(got, want, tol, ("dQ", "dK", "dV")):
+        _within(g, w, t, name)
+    assert all(bool(torch.isfinite(x).all()) for x in held)
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("B,H", [(0, 3), (2, 0)])
+def test_no_batch_or_no_head(B, H, dtype):
+    csa = _csa()
+    q = torch.zeros(B, H, 5, 64, dtype=dtype, device="cuda")
+    k = torch.zeros(B, H, 9, 64, dtype=dtype, device="cuda")
+    O, lse = csa.svgear_cross_attend(q, k, k)
+    grads = csa.svgear_cross_attend_backward(q, q, k, k, O, lse)
+    c = csa.svgear_checkpoint_save(q)
+    grads += csa.svgear_cross_attend_backward_ckpt(q, c, k, k, c, lse)
+    assert O.shape == q.shape and lse.shape == q.shape[:3]
+    assert [tuple(x.shape) for x in grads] == [tuple(x.shape) for x in (q, k, k)] * 2
+    assert csa.svgear_checkpoint_load(c).shape == q.shape
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+def test_keys_as_values_and_queries(dtype):
+    """The same tensor in every place it may take."""
+    csa = _csa()
+    x, _, _, do = _inputs(43, 2, 3, 3, 150, 150, 64, dtype)
+    O, lse = _check_forward(x, x, x, [150, 31], 0.125)
+    _check_backward(do, x, x, x, O, lse, [150, 31], 0.125)
+
+
 def test_a_training_step_beside_the_clustered_layer():
     """The operators as a block uses them: clustered self-attention, its output
     as the queries of a cross attention to padded prompts, activations held in
