@@ -623,6 +623,12 @@ def _view(t, name, like=None, shape=None):
     return Tokens(t.data_ptr(), st[0], st[1], st[2])
 
 
+def _made(t):
+    """A tensor of _new_like as a Tokens struct."""
+    st = t.stride()
+    return Tokens(t.data_ptr(), st[0], st[1], st[2])
+
+
 def _dense(t, name, dtype, device, shape):
     if not (t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.device == device):
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
@@ -657,16 +663,16 @@ def _cross_dims(q_shape, K, k_len):
         raise ValueError("K must have the shape [%d, Hkv, Nk, %d], not %s" % (B, d, tuple(ks)))
     if k_len is not None:
         _dense(k_len, "k_len", torch.int32, K.device, (B,))
-    return CrossDims(B, Hq, ks[1], Nq, ks[2], d, _dtype_code(K))
+    return B, Hq, ks[1], Nq, ks[2], d, _dtype_code(K)
 
 
 @functools.lru_cache(maxsize=4096)
-def _cross_bytes(op, *dims):
+def _cross_bytes(op, dims):
     return max(int(lib().svgear_cross_workspace_bytes(op, CrossDims(*dims))), 256)
 
 
-def _cross_workspace(op, d, device):
-    n = _cross_bytes(op, d.B, d.Hq, d.Hkv, d.Nq, d.Nk, d.d, d.dtype)
+def _cross_workspace(op, dims, device):
+    n = _cross_bytes(op, dims)
     return torch.empty(n, dtype=torch.uint8, device=device), n
 
 
@@ -682,14 +688,16 @@ def svgear_cross_attend(Q, K, V, scale=None, k_len=None, O=None, lse=None, check
     dims = _cross_dims(Q.shape, K, k_len)
     if O is None:
         O = _new_like(Q)
-    o = _view(O, "O", Q, Q.shape)
+        o = _made(O)
+    else:
+        o = _view(O, "O", Q, Q.shape)
     if lse is None:
-        lse = Q.new_empty((dims.B, dims.Hq, dims.Nq), dtype=torch.float32)
+        lse = Q.new_empty((dims[0], dims[1], dims[3]), dtype=torch.float32)
     else:
         _dense(lse, "lse", torch.float32, Q.device, Q.shape[:3])
     ws, n = _cross_workspace(CROSS_FORWARD, dims, Q.device)
     _check("svgear_cross_attend", lib().svgear_cross_attend(
-        q, k, v, dims, _ptr(k_len), float(dims.d ** -0.5 if scale is None else scale), o,
+        q, k, v, CrossDims(*dims), _ptr(k_len), float(Q.shape[3] ** -0.5 if scale is None else scale), o,
         lse.data_ptr(), ws.data_ptr(), n, _raw_stream(Q.device)))
     if check_status:
         _device_status("svgear_cross_attend", ws, n)
@@ -707,9 +715,8 @@ def svgear_cross_attend_backward(dO, Q, K, V, O, lse, scale=None, k_len=None, ch
     dQ, dK, dV = _new_like(Q), _new_like(K), _new_like(V)
     ws, n = _cross_workspace(CROSS_BACKWARD, dims, Q.device)
     _check("svgear_cross_attend_backward", lib().svgear_cross_attend_backward(
-        g, q, k, v, o, lse.data_ptr(), dims, _ptr(k_len),
-        float(dims.d ** -0.5 if scale is None else scale), _view(dQ, "dQ"), _view(dK, "dK"),
-        _view(dV, "dV"), ws.data_ptr(), n, _raw_stream(Q.device)))
+        g, q, k, v, o, lse.data_ptr(), CrossDims(*dims), _ptr(k_len),
+        float(Q.shape[3] ** -0.5 if scale is None else scale), _made(dQ), _made(dK), _made(dV), ws.data_ptr(), n, _raw_stream(Q.device)))
     if check_status:
         _device_status("svgear_cross_attend_backward", ws, n)
     return dQ, dK, dV
@@ -769,9 +776,8 @@ def svgear_cross_attend_backward_ckpt(dO, Qc, K, V, Oc, lse, scale=None, k_len=N
     dQ, dK, dV = _new_like(dO), _new_like(K), _new_like(V)
     ws, n = _cross_workspace(CROSS_BACKWARD_CKPT, dims, dO.device)
     _check("svgear_cross_attend_backward_ckpt", lib().svgear_cross_attend_backward_ckpt(
-        g, qc, qe, k, v, oc, oe, lse.data_ptr(), dims, _ptr(k_len),
-        float(dims.d ** -0.5 if scale is None else scale), _view(dQ, "dQ"), _view(dK, "dK"),
-        _view(dV, "dV"), ws.data_ptr(), n, _raw_stream(dO.device)))
+        g, qc, qe, k, v, oc, oe, lse.data_ptr(), CrossDims(*dims), _ptr(k_len),
+        float(dO.shape[3] ** -0.5 if scale is None else scale), _made(dQ), _made(dK), _made(dV), ws.data_ptr(), n, _raw_stream(dO.device)))
     if check_status:
         _device_status("svgear_cross_attend_backward_ckpt", ws, n)
     return dQ, dK, dV

@@ -385,6 +385,10 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             c0 *= inv;
             c1 *= inv;
+            if (write) {
+                const float lse = sum == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(sum));
+                (parts ? lse_part[part] : a.lse[rr]) = lse;
+            }
             if (!warp_poll_bar(&sh.o_full, n & 1, abort_flag, err, (15 << 16))) break;
             tc::fence_after_sync();
             // 32 columns of both accumulators at a time (beside running MMAs a
@@ -430,11 +434,6 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
             }
             __syncwarp();
             ++n;
-            if (write) {
-                const float lse = sum == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(sum));
-                if (parts) lse_part[part] = lse;
-                else a.lse[rr] = lse;
-            }
         }
     }
     __syncwarp();
