@@ -86,12 +86,32 @@ __device__ __forceinline__ void dot_tile(const float* A, const float* Bm, int va
     else dot_columns<D, 4>(A, Bm, ty, tx, acc);
 }
 
-// acc[i][4 c + e] += sum_n W[ty + 8 i][n] X[n][64 c + 4 tx + e]; W rows of N + 4,
+// A product with a tile's weights is summed on its own and then added to the
+// running sum: n terms then take chains of 64 and n / 64 additions.  In one chain of
+// n the error of equal terms does not cancel (O over 75,600 equal keys: off by 9e-4,
+// now within 1e-5), and the additions saved are 1 in 64.
+template <int C>
+__device__ __forceinline__ void clear(float (&x)[R][C]) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int c = 0; c < C; ++c) x[i][c] = 0.f;
+}
+template <int C>
+__device__ __forceinline__ void add(float (&acc)[R][C], const float (&x)[R][C]) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[i][c] += x[i][c];
+}
+
+// acc[i][4 c + e] = sum_n W[ty + 8 i][n] X[n][64 c + 4 tx + e]; W rows of N + 4,
 // X rows of D + 4, n < valid (weights past it are 0); C columns (a multiple of
 // 64, or 32: then two per thread)
 template <int D, int C = D>
-__device__ __forceinline__ void accumulate(const float* W, const float* X, int valid, int ty, int tx,
-                                           float (&acc)[R][C / 16]) {
+__device__ __forceinline__ void tile_product(const float* W, const float* X, int valid, int ty, int tx,
+                                             float (&acc)[R][C / 16]) {
+    clear(acc);
 #pragma unroll 2
     for (int n = 0; n < min(N, valid); n += 4) {
         float4 w[R];
@@ -125,10 +145,11 @@ __device__ __forceinline__ void accumulate(const float* W, const float* X, int v
     }
 }
 
-// acc[i][4 c + e] += sum_q W[q][8 ty + i] X[q][64 c + 4 tx + e] (W transposed)
+// acc[i][4 c + e] = sum_q W[q][8 ty + i] X[q][64 c + 4 tx + e] (W transposed)
 template <int D>
-__device__ __forceinline__ void accumulate_t(const float* W, const float* X, int ty, int tx,
-                                             float (&acc)[R][D / 16]) {
+__device__ __forceinline__ void tile_product_t(const float* W, const float* X, int ty, int tx,
+                                               float (&acc)[R][D / 16]) {
+    clear(acc);
 #pragma unroll 4
     for (int q = 0; q < M; ++q) {
         const float4 w = *reinterpret_cast<const float4*>(W + q * (N + 4) + 8 * ty);
@@ -192,12 +213,11 @@ cross_fwd_kernel(CrossArgs a, int splits, int tiles_per_split, float* __restrict
 
     copy_tile<D>(sQ, a.Q, b, h, q0, a.Nq);
     float m[R], l[R], o[R][D / 16];
+    clear(o);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
     }
     for (int t = t0; t < t1; ++t) {
         __syncthreads();
@@ -221,19 +241,22 @@ cross_fwd_kernel(CrossArgs a, int splits, int tiles_per_split, float* __restrict
             const float mu = mn == -INFINITY ? 0.f : mn;   // every score -inf so far
             const float alpha = expf(m[i] - mu);
             m[i] = mn;
-            l[i] *= alpha;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) o[i][c] *= alpha;
+            float lt = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float p = expf(s[i][j] - mu);
-                l[i] += p;
+                lt += p;
                 sP[(ty + 8 * i) * (N + 4) + tx + 16 * j] = p;
             }
+            l[i] = fmaf(l[i], alpha, lt);
         }
         tc::cp_async_wait<0>();
         __syncthreads();
-        accumulate<D>(sP, sV, keys - t * N, ty, tx, o);
+        float x[R][D / 16];
+        tile_product<D>(sP, sV, keys - t * N, ty, tx, x);
+        add(o, x);
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -328,7 +351,7 @@ __device__ __forceinline__ void put_score_grads(const float (&dp)[R][4], const f
         }
 }
 
-// a thread's columns of a row of C, as accumulate() has them, times f
+// a thread's columns of a row of C, as tile_product() has them, times f
 template <int C>
 __device__ __forceinline__ void store_half(float* dst, const float (&x)[C / 16], float f, int tx) {
     if constexpr (C == 64)
@@ -361,10 +384,7 @@ __global__ void __launch_bounds__(kGradThreads) cross_dq_kernel(CrossArgs a) {
         s_delta[threadIdx.x] = row < a.Nq ? a.delta[r] : 0.f;
     }
     float dq[R][C / 16];
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int c = 0; c < C / 16; ++c) dq[i][c] = 0.f;
+    clear(dq);
     for (int t = 0; t * N < keys; ++t) {
         float* sK = sKV + (t & 1) * 2 * N * (D + 4);
         float* sV = sK + N * (D + 4);
@@ -382,7 +402,9 @@ __global__ void __launch_bounds__(kGradThreads) cross_dq_kernel(CrossArgs a) {
         __syncthreads();
         if (grp == 1) put_score_grads(s, s_delta, sS, sS, ty, tx);
         __syncthreads();
-        accumulate<D, C>(sS, sK + grp * C, keys - t * N, ty, tx, dq);
+        float x[R][C / 16];
+        tile_product<D, C>(sS, sK + grp * C, keys - t * N, ty, tx, x);
+        add(dq, x);
     }
     tc::cp_async_wait<0>();
 #pragma unroll
@@ -426,10 +448,7 @@ __global__ void __launch_bounds__(kGradThreads) cross_dkv_kernel(CrossArgs a, fl
         copy_q(first);
         tc::cp_async_commit();
         float acc[R][D / 16];   // group 0: dV, group 1: dK
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
+        clear(acc);
         for (int64_t x = first; x < last; ++x) {
             const int g = (int)(x / qtiles), q0 = (int)(x - (int64_t)g * qtiles) * M;
             const int h = k.h * a.G + g;
@@ -451,23 +470,26 @@ __global__ void __launch_bounds__(kGradThreads) cross_dkv_kernel(CrossArgs a, fl
             dot_tile<D>(grp ? sG : sQ, grp ? sV : sK, valid, ty, tx, s);
             if (grp == 0) put_weights(s, s_lse, sP, ty, tx, k.kt * N, k.keys, a.scale);
             __syncthreads();
+            float y[R][D / 16];
             if (grp == 0) {
-                if (8 * ty < valid) accumulate_t<D>(sP, sG, ty, tx, acc);   // rows past the keys are not written
+                if (8 * ty < valid) {   // rows past the keys are not written
+                    tile_product_t<D>(sP, sG, ty, tx, y);
+                    add(acc, y);
+                }
                 if constexpr (DQ) asm volatile("bar.sync 2, 256;" ::: "memory");   // ds from group 1
             } else {
                 put_score_grads(s, s_delta, sP, sS, ty, tx);
                 asm volatile("bar.sync 1, 128;" ::: "memory");   // group 1
                 if constexpr (DQ) asm volatile("bar.arrive 2, 256;" ::: "memory");
-                if (8 * ty < valid) accumulate_t<D>(sS, sQ, ty, tx, acc);
+                if (8 * ty < valid) {
+                    tile_product_t<D>(sS, sQ, ty, tx, y);
+                    add(acc, y);
+                }
             }
             if constexpr (DQ) {
                 constexpr int C = D / 2;
                 float dq[R][C / 16];
-#pragma unroll
-                for (int i = 0; i < R; ++i)
-#pragma unroll
-                    for (int c = 0; c < C / 16; ++c) dq[i][c] = 0.f;
-                accumulate<D, C>(sS, sK + grp * C, valid, ty, tx, dq);
+                tile_product<D, C>(sS, sK + grp * C, valid, ty, tx, dq);
                 float* pq = a.dq_part + (((size_t)k.kt * a.B + k.b) * a.Hq + h) * a.Nq * D + grp * C;
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
