@@ -326,8 +326,10 @@ cross_fwd_sm100_kernel(const __grid_constant__ Maps maps, CrossArgs a, Plan plan
                         pk[e >> 1] = bf16_pair(p0, p1);
                     }
                     // P(g - 2) must have been read out of the buffer
-                    if (q == 0 && g >= 2)
+                    if (q == 0 && g >= 2) {
                         ok = warp_poll_bar(&sh.p_free[b], ((g >> 1) - 1) & 1, abort_flag, err, (11 << 16));
+                        tc::fence_after_sync();   // its MMA's reads before the stores below
+                    }
                     tc::tmem_st16(tP + q * 16, pk);
                 }
                 if (!ok) break;

@@ -181,3 +181,37 @@ def test_dkv_barriers_never_lap(iterations):
     assert cross_protocol.stuck_states(iterations, int(m.group(2) or 1)) == []
     if iterations > 1:
         assert cross_protocol.stuck_states(iterations, 1)   # the model sees the fault
+
+
+TMEM_ACCESS = re.compile(r"\b(tmem_ld\d+|tmem_st\d+|mask_columns<|mma_\w+<|issue_s\(\);|issue_dp\(\);)")
+
+
+def unfenced_accesses(source):
+    """Accesses to tensor memory (products, loads, stores) that follow a barrier wait of the
+    same thread without tcgen05.fence::after_thread_sync in between: line numbers."""
+    waited, bad = False, []
+    for n, line in enumerate(source.splitlines(), 1):
+        line = line.split("//")[0]
+        if "auto issue_" in line:       # a lambda: its calls are looked at, not its body
+            waited = False
+        if "fence_after_sync()" in line:
+            waited = False
+        if "poll_bar(" in line or "drain_bar(" in line:
+            waited = True
+        if waited and TMEM_ACCESS.search(line):
+            bad.append(n)
+    return bad
+
+
+@pytest.mark.parametrize("name", ["cross_sm100.cu", "cross_bwd_sm100.cu"])
+def test_tensor_memory_is_fenced_after_every_wait(name):
+    """A barrier orders tensor-memory accesses of two threads only together with the fence
+    behind the wait."""
+    src = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       "clustered_sparse_attention_b200", "csrc", name)
+    with open(src) as f:
+        text = f.read()
+    assert text.count("poll_bar(") > 10 and unfenced_accesses(text) == []
+    # the scan sees the fault: without the first fence behind a wait
+    at = text.index("fence_after_sync()", text.index("poll_bar("))
+    assert unfenced_accesses(text[:at] + text[at + len("fence_after_sync()"):])
