@@ -642,18 +642,20 @@ def _new_like(t):
     return out if out.stride(-1) == 1 else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-def _on_device(fn):
-    """Runs a call with the device of its first argument as the current one."""
-    @functools.wraps(fn)
-    def call(*args, **kw):
-        t = args[0] if args else next(iter(kw.values()), None)
-        t = t.codes if isinstance(t, Checkpoint) else t
-        if (not isinstance(t, torch.Tensor) or not t.is_cuda
-                or t.device.index == torch.cuda.current_device()):
-            return fn(*args, **kw)
-        with torch.cuda.device(t.device):
-            return fn(*args, **kw)
-    return call
+def _on_device(name):
+    """Runs a call with the device of its first argument, `name`, as the current
+    one, in whatever order the arguments come by name."""
+    def wrap(fn):
+        @functools.wraps(fn)
+        def call(*args, **kw):
+            t = args[0] if args else kw.get(name)
+            t = t.codes if isinstance(t, Checkpoint) else t
+            if not getattr(t, "is_cuda", False) or t.device.index == torch.cuda.current_device():
+                return fn(*args, **kw)
+            with torch.cuda.device(t.device):
+                return fn(*args, **kw)
+        return call
+    return wrap
 
 
 def _cross_dims(q_shape, K, k_len):
@@ -676,7 +678,7 @@ def _cross_workspace(op, dims, device):
     return torch.empty(n, dtype=torch.uint8, device=device), n
 
 
-@_on_device
+@_on_device("Q")
 def svgear_cross_attend(Q, K, V, scale=None, k_len=None, O=None, lse=None, check_status=False):
     """Attention of Q [B, Hq, Nq, d] over an encoder's states K, V
     [B, Hkv, Nk, d], Hkv dividing Hq, over the first k_len[b] keys (int32 [B];
@@ -704,7 +706,7 @@ def svgear_cross_attend(Q, K, V, scale=None, k_len=None, O=None, lse=None, check
     return O, lse
 
 
-@_on_device
+@_on_device("dO")
 def svgear_cross_attend_backward(dO, Q, K, V, O, lse, scale=None, k_len=None, check_status=False):
     """Gradients (dQ, dK, dV) of svgear_cross_attend's O, given its O and lse
     and the gradient dO; each of its input's type and layout."""
@@ -722,7 +724,7 @@ def svgear_cross_attend_backward(dO, Q, K, V, O, lse, scale=None, k_len=None, ch
     return dQ, dK, dV
 
 
-@_on_device
+@_on_device("X")
 def svgear_checkpoint_save(X):
     """X [B, H, N, d] (strided, d contiguous) in 8 bits: a Checkpoint."""
     x = _view(X, "X")
@@ -747,7 +749,7 @@ def _held(c, name, shape=None, device=None, dtype=None):
     return c.codes.data_ptr(), c.exps.data_ptr()
 
 
-@_on_device
+@_on_device("c")
 def svgear_checkpoint_load(c, out=None):
     """The tensor a Checkpoint stands for, in its type; dense unless `out`."""
     codes, exps = _held(c, "c")
@@ -763,7 +765,7 @@ def svgear_checkpoint_load(c, out=None):
     return out
 
 
-@_on_device
+@_on_device("dO")
 def svgear_cross_attend_backward_ckpt(dO, Qc, K, V, Oc, lse, scale=None, k_len=None,
                                       check_status=False):
     """svgear_cross_attend_backward with Q and O read from Checkpoints."""

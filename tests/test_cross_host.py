@@ -2,6 +2,7 @@
 call below reaches the GPU), and of the tests' 64-bit forms against
 differences."""
 import ctypes
+import inspect
 import os
 import re
 
@@ -128,6 +129,61 @@ def test_binding_refuses_before_any_call():
         csa.svgear_checkpoint_load(csa.Checkpoint(torch.zeros(1, 2, 4, 64, dtype=torch.int8),
                                                   torch.zeros(1, 2, 4, 2, dtype=torch.uint8),
                                                   torch.float32))
+
+
+@pytest.mark.parametrize("fn", ["svgear_cross_attend", "svgear_cross_attend_backward",
+                                "svgear_cross_attend_backward_ckpt", "svgear_checkpoint_save",
+                                "svgear_checkpoint_load"])
+def test_calls_run_on_their_tensors_device(fn, monkeypatch):
+    """Whichever way the arguments come, with another device than theirs current."""
+    import clustered_sparse_attention_b200 as csa
+    from clustered_sparse_attention_b200 import _lib
+
+    class Reached(Exception):
+        pass
+
+    class Tensor:                       # as much of one as is looked at before the call
+        is_cuda, device, dtype = True, torch.device("cuda", 1), torch.bfloat16
+        shape = torch.Size((1, 2, 4, 64))
+
+        def stride(self):
+            raise Reached
+
+        dim = stride
+
+    entered = []
+
+    class Device:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            entered.append(self.d)
+
+        def __exit__(self, *exc):
+            return False
+
+    monkeypatch.setattr(_lib.torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(_lib.torch.cuda, "device", Device)
+    call = getattr(csa, fn)
+    t = Tensor()
+    tensor = csa.Checkpoint(t, t, t.dtype) if fn == "svgear_checkpoint_load" else t
+    names = list(inspect.signature(call).parameters)
+    needed = {n: t for n in names if n in ("dO", "Q", "K", "V", "O", "lse", "Qc", "Oc")}
+    needed[names[0]] = tensor
+    last = dict(reversed(list(needed.items())))         # the first argument at the end
+    optional = {n: None for n in names if n in ("scale", "k_len", "out")}
+    for args, kw in (((tensor,), {n: x for n, x in needed.items() if n != names[0]}),
+                     ((), needed), ((), {**optional, **last})):
+        entered.clear()
+        with pytest.raises(Reached):
+            call(*args, **kw)
+        assert entered == [t.device]
+        Tensor.device = torch.device("cuda", 0)         # the current one: nothing to switch
+        with pytest.raises(Reached):
+            call(*args, **kw)
+        assert entered == [torch.device("cuda", 1)]
+        Tensor.device = torch.device("cuda", 1)
 
 
 def test_oracle_gradients_match_differences():
