@@ -160,10 +160,15 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+# The current stream's handle without a Stream object, which takes 3.4 us of a call
+# against 0.3; not a public function, so the public one stands in where it is missing.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(device):
-    """The current stream's handle; the public accessor builds a Stream object
-    first (3.4 us against 0.3)."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    if _current_raw_stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _current_raw_stream(device.index)
 
 
 def _dtype_code(t):

@@ -186,6 +186,16 @@ def test_calls_run_on_their_tensors_device(fn, monkeypatch):
         Tensor.device = torch.device("cuda", 1)
 
 
+def test_current_stream_without_the_private_function(monkeypatch):
+    from types import SimpleNamespace
+    from clustered_sparse_attention_b200 import _lib
+    dev = torch.device("cuda", 3)
+    monkeypatch.setattr(_lib, "_current_raw_stream", None)
+    monkeypatch.setattr(_lib.torch.cuda, "current_stream",
+                        lambda d: SimpleNamespace(cuda_stream=1000 + d.index))
+    assert _lib._raw_stream(dev) == 1003
+
+
 def test_oracle_gradients_match_differences():
     g = torch.Generator().manual_seed(3)
     q = torch.randn(2, 4, 3, 8, generator=g, dtype=torch.float64)
