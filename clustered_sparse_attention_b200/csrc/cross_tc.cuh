@@ -1,6 +1,7 @@
-// cross_tc.cuh -- what the tcgen05 kernels of the cross attention share:
-// tensor maps of strided token views and the copy of a key tile whose rows
-// past the batch's key count must read as zeros.
+// cross_tc.cuh -- what the tcgen05 kernels of the cross attention share: their PTX
+// wrappers and waits beside those of tc_ptx.cuh and tc_wait.cuh, tensor maps of
+// strided token views and the copy of a key tile whose rows past the batch's key
+// count must read as zeros.
 #pragma once
 
 #include <atomic>
@@ -13,6 +14,169 @@
 #include "tma_host.h"
 
 namespace svgear {
+
+namespace tc {
+
+// 4-D tile load of the tensor map's box at (x, y, z, w).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int x, int y, int z,
+                                            int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+// The same box brought into L2 only.
+__device__ __forceinline__ void tma_prefetch_4d(const void* tmap, int x, int y, int z, int w) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                     reinterpret_cast<uint64_t>(tmap)),
+                 "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+
+// Writes the tensor map's box from shared memory to (x, y, z, w); rows past the
+// tensor are left out.  Part of the issuing thread's current bulk group.
+__device__ __forceinline__ void tma_store_4d(const void* tmap, uint32_t src, int x, int y, int z,
+                                             int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+            reinterpret_cast<uint64_t>(tmap)),
+        "r"(x), "r"(y), "r"(z), "r"(w), "r"(src)
+        : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Until this thread's bulk groups have read shared memory.
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
+// The first four steps of mma_bf16_ts_k128.
+__device__ __forceinline__ void mma_bf16_ts_k64(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                                uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 t;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "add.u32 t, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
+        "add.u32 t, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
+        "add.u32 t, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(1u)
+        : "memory");
+}
+
+// As mma_bf16_ts_k128 with the A operand in two runs of 32 columns, the second
+// 64 columns after the first (each run 64 K elements).
+__device__ __forceinline__ void mma_bf16_ts_2k64(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                                 uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 t;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "add.u32 t, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
+        "add.u32 t, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
+        "add.u32 t, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
+        "add.u32 t, %1, 64;\n\tadd.s64 b, %2, 512;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
+        "add.u32 t, %1, 72;\n\tadd.s64 b, %2, 640;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
+        "add.u32 t, %1, 80;\n\tadd.s64 b, %2, 768;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
+        "add.u32 t, %1, 88;\n\tadd.s64 b, %2, 896;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(1u)
+        : "memory");
+}
+
+// As wait_bar, for loops whose waits last a few thousand cycles and whose
+// latency counts: the abort flags and the clock are read every 1024 polls (some
+// 30,000 cycles).  Reading the status word and %globaltimer takes long enough
+// that a barrier completed meanwhile goes unseen on the critical path (cross
+// attention forward, 75,600 x 512 keys: 930 us with a look every 64 polls, 873
+// with this).
+// The slow look, one copy for all waits of a kernel (inlined, it made up a third
+// of its code).  Returns true to go on polling; *t0 is the first look's time.
+static __device__ __noinline__ bool poll_look(uint64_t* t0, volatile int* abort_flag, int* err, int where,
+                                              uint32_t it) {
+    if (*abort_flag || *(volatile int*)err) {
+        *abort_flag = 1;
+        return false;
+    }
+    const uint64_t now = global_timer_ns();
+    if (*t0 == 0) *t0 = now;
+    if (now - *t0 > kWaitTimeoutNs || it >= kMaxSpins) {
+        *abort_flag = 1;
+        if (atomicCAS(err, 0, SVGEAR_ERR_TIMEOUT) == 0) {
+            err[1] = where;
+            err[2] = (int)(blockIdx.y * 65536 + blockIdx.x);
+        }
+        return false;
+    }
+    return true;
+}
+__device__ __forceinline__ bool poll_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                         int* err, int where) {
+    const uint32_t b = smem_u32(bar);
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(b, parity)) return true;
+        if ((it & 1023) == 0 && !poll_look(&t0, abort_flag, err, where, it)) return false;
+    }
+}
+// For a whole warp: every lane polls (one shared-memory access for all, and no
+// divergence to undo), and all get the same answer.
+__device__ __forceinline__ bool warp_poll_bar(uint64_t* bar, uint32_t parity,
+                                              volatile int* abort_flag, int* err, int where) {
+    return __all_sync(0xffffffffu, poll_bar(bar, parity, abort_flag, err, where)) != 0;
+}
+
+// As wait_bar for copies or MMAs already issued, while a kernel gives up: it
+// ignores the abort flags and only the clock ends it.
+__device__ __forceinline__ bool drain_bar(uint64_t* bar, uint32_t parity) {
+    const uint32_t b = smem_u32(bar);
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 0; it < kMaxSpins; ++it) {
+        if (mbar_try_wait(b, parity)) return true;
+        if ((it & 63) == 63 && global_timer_ns() - t0 > kWaitTimeoutNs) return false;
+    }
+    return false;
+}
+
+}  // namespace tc
+
+// A strided bf16 token view [B][H][N][D] as 4-D boxes of 64 columns x box_rows
+// rows of one (b, h), 128-byte swizzled; rows past N read as zeros.  An axis
+// whose stride is 0 (length 1, or broadcast) is an axis of length 1: its
+// coordinate is 0.
+inline bool make_tokens_map(CUtensorMap* m, const svgear_tokens& t, int B, int H, int N, int D,
+                            uint32_t box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const int64_t st[3] = {t.stride_n, t.stride_h, t.stride_b};
+    const int len[3] = {N, H, B};
+    cuuint64_t dims[4] = {(cuuint64_t)D, 1, 1, 1};
+    cuuint64_t strides[3];
+    for (int i = 0; i < 3; ++i) {
+        dims[i + 1] = st[i] ? (cuuint64_t)len[i] : 1;
+        strides[i] = (cuuint64_t)(st[i] ? st[i] : D) * 2;
+    }
+    cuuint32_t box[4] = {64, box_rows, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t.data, dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace crosstc {
 
 constexpr int BM = 128;   // query rows per tile

@@ -117,22 +117,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int 
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
-// 4-D tile load of the tensor map's box at (x, y, z, w).
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int x, int y, int z,
-                                            int w, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-        : "memory");
-}
-// The same box brought into L2 only.
-__device__ __forceinline__ void tma_prefetch_4d(const void* tmap, int x, int y, int z, int w) {
-    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
-                     reinterpret_cast<uint64_t>(tmap)),
-                 "r"(x), "r"(y), "r"(z), "r"(w)
-                 : "memory");
-}
 // Four rows y0..y3 (box one row high, columns x..x+box) into 4 consecutive
 // rows of shared memory at dst.
 __device__ __forceinline__ void tma_gather4(uint32_t dst, const void* tmap, int x, int y0, int y1,
@@ -143,24 +127,6 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const void* tmap, int 
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3),
         "r"(bar)
         : "memory");
-}
-
-// Writes the tensor map's box from shared memory to (x, y, z, w); rows past the
-// tensor are left out.  Part of the issuing thread's current bulk group.
-__device__ __forceinline__ void tma_store_4d(const void* tmap, uint32_t src, int x, int y, int z,
-                                             int w) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
-            reinterpret_cast<uint64_t>(tmap)),
-        "r"(x), "r"(y), "r"(z), "r"(w), "r"(src)
-        : "memory");
-}
-__device__ __forceinline__ void bulk_commit() {
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// Until this thread's bulk groups have read shared memory.
-__device__ __forceinline__ void bulk_wait_read() {
-    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // ---- tcgen05 ---------------------------------------------------------------
@@ -266,51 +232,6 @@ __device__ __forceinline__ void mma_bf16_ts_k128(uint32_t d_tmem, uint32_t a_tme
         "add.u32 t, %1, 48;\n\tadd.s64 b, %2, 768;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
         "add.u32 t, %1, 56;\n\tadd.s64 b, %2, 896;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(1u)
-        : "memory");
-}
-
-// The first four steps of mma_bf16_ts_k128.
-__device__ __forceinline__ void mma_bf16_ts_k64(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                                uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b32 t;\n\t.reg .b64 b;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-        "add.u32 t, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
-        "add.u32 t, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
-        "add.u32 t, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(1u)
-        : "memory");
-}
-
-// As mma_bf16_ts_k128 with the A operand in two runs of 32 columns, the second
-// 64 columns after the first (each run 64 K elements).
-__device__ __forceinline__ void mma_bf16_ts_2k64(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                                 uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b32 t;\n\t.reg .b64 b;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-        "add.u32 t, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
-        "add.u32 t, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
-        "add.u32 t, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
-        "add.u32 t, %1, 64;\n\tadd.s64 b, %2, 512;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
-        "add.u32 t, %1, 72;\n\tadd.s64 b, %2, 640;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
-        "add.u32 t, %1, 80;\n\tadd.s64 b, %2, 768;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t"
-        "add.u32 t, %1, 88;\n\tadd.s64 b, %2, 896;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, q;\n\t}\n" ::"r"(d_tmem),
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(1u)
         : "memory");

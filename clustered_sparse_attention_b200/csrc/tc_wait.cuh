@@ -49,61 +49,6 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
     }
 }
 
-// As wait_bar, for loops whose waits last a few thousand cycles and whose
-// latency counts: the abort flags and the clock are read every 1024 polls (some
-// 30,000 cycles).  Reading the status word and %globaltimer takes long enough
-// that a barrier completed meanwhile goes unseen on the critical path (cross
-// attention forward, 75,600 x 512 keys: 930 us with a look every 64 polls, 873
-// with this).
-// The slow look, one copy for all waits of a kernel (inlined, it made up a third
-// of its code).  Returns true to go on polling; *t0 is the first look's time.
-static __device__ __noinline__ bool poll_look(uint64_t* t0, volatile int* abort_flag, int* err, int where,
-                                              uint32_t it) {
-    if (*abort_flag || *(volatile int*)err) {
-        *abort_flag = 1;
-        return false;
-    }
-    const uint64_t now = global_timer_ns();
-    if (*t0 == 0) *t0 = now;
-    if (now - *t0 > kWaitTimeoutNs || it >= kMaxSpins) {
-        *abort_flag = 1;
-        if (atomicCAS(err, 0, SVGEAR_ERR_TIMEOUT) == 0) {
-            err[1] = where;
-            err[2] = (int)(blockIdx.y * 65536 + blockIdx.x);
-        }
-        return false;
-    }
-    return true;
-}
-__device__ __forceinline__ bool poll_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                         int* err, int where) {
-    const uint32_t b = smem_u32(bar);
-    uint64_t t0 = 0;
-#pragma unroll 1
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(b, parity)) return true;
-        if ((it & 1023) == 0 && !poll_look(&t0, abort_flag, err, where, it)) return false;
-    }
-}
-// For a whole warp: every lane polls (one shared-memory access for all, and no
-// divergence to undo), and all get the same answer.
-__device__ __forceinline__ bool warp_poll_bar(uint64_t* bar, uint32_t parity,
-                                              volatile int* abort_flag, int* err, int where) {
-    return __all_sync(0xffffffffu, poll_bar(bar, parity, abort_flag, err, where)) != 0;
-}
-
-// As wait_bar for copies or MMAs already issued, while a kernel gives up: it
-// ignores the abort flags and only the clock ends it.
-__device__ __forceinline__ bool drain_bar(uint64_t* bar, uint32_t parity) {
-    const uint32_t b = smem_u32(bar);
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t it = 0; it < kMaxSpins; ++it) {
-        if (mbar_try_wait(b, parity)) return true;
-        if ((it & 63) == 63 && global_timer_ns() - t0 > kWaitTimeoutNs) return false;
-    }
-    return false;
-}
-
 // The device's tensor-memory-lost word (guard.cu): set by a kernel that kept
 // its TMEM columns because an MMA it issued may still have been running.
 __device__ __forceinline__ void mark_tmem_lost(int* lost) {

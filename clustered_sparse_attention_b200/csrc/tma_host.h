@@ -9,8 +9,6 @@
 
 #include <mutex>
 
-#include "svgear.h"
-
 namespace svgear {
 
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -39,29 +37,6 @@ inline bool make_rows_map(CUtensorMap* m, const void* base, uint64_t rows, int D
     cuuint32_t estr[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// A strided bf16 token view [B][H][N][D] as 4-D boxes of 64 columns x box_rows
-// rows of one (b, h), 128-byte swizzled; rows past N read as zeros.  An axis
-// whose stride is 0 (length 1, or broadcast) is an axis of length 1: its
-// coordinate is 0.
-inline bool make_tokens_map(CUtensorMap* m, const svgear_tokens& t, int B, int H, int N, int D,
-                            uint32_t box_rows) {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    if (!enc) return false;
-    const int64_t st[3] = {t.stride_n, t.stride_h, t.stride_b};
-    const int len[3] = {N, H, B};
-    cuuint64_t dims[4] = {(cuuint64_t)D, 1, 1, 1};
-    cuuint64_t strides[3];
-    for (int i = 0; i < 3; ++i) {
-        dims[i + 1] = st[i] ? (cuuint64_t)len[i] : 1;
-        strides[i] = (cuuint64_t)(st[i] ? st[i] : D) * 2;
-    }
-    cuuint32_t box[4] = {64, box_rows, 1, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t.data, dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
