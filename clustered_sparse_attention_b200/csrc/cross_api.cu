@@ -86,6 +86,12 @@ CrossArgs make_args(const svgear_cross_dims& d, const int32_t* k_len, float scal
     return a;
 }
 
+// Addresses that the kernels' loads and stores would fault on.
+bool aligned(const void* p, uintptr_t bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
+bool bad_buffers(const float* lse, const int32_t* k_len, const void* ws) {
+    return !aligned(lse, sizeof(float)) || !aligned(k_len, sizeof(int32_t)) || !ws || !aligned(ws, 16);
+}
+
 bool bad_scale(float scale) { return !(scale > 0.f) || !isfinite(scale * 1.4426950408889634f); }
 
 size_t rows_of(const svgear_cross_dims& d) { return (size_t)d.B * d.Hq * d.Nq; }
@@ -149,7 +155,7 @@ int backward(svgear_tokens dO, svgear_tokens Q, const HeldTokens* qh, svgear_tok
         (s = check_view(dV, B, Hkv, Nk, dims.d, dims.dtype, true)))
         return s;
     const bool none = B == 0 || Hq == 0;
-    if ((!lse && !none) || !ws || bad_scale(scale)) return SVGEAR_ERR_INVALID_ARG;
+    if ((!lse && !none) || bad_buffers(lse, k_len, ws) || bad_scale(scale)) return SVGEAR_ERR_INVALID_ARG;
     if (ws_bytes < svgear_cross_workspace_bytes(
                        qh ? SVGEAR_CROSS_BACKWARD_CKPT : SVGEAR_CROSS_BACKWARD, dims))
         return SVGEAR_ERR_WORKSPACE;
@@ -210,7 +216,7 @@ int svgear_cross_attend(svgear_tokens Q, svgear_tokens K, svgear_tokens V, svgea
         (s = check_view(O, dims.B, dims.Hq, dims.Nq, dims.d, dims.dtype, true)))
         return s;
     const bool none = dims.B == 0 || dims.Hq == 0;
-    if ((!lse && !none) || !ws || bad_scale(scale)) return SVGEAR_ERR_INVALID_ARG;
+    if ((!lse && !none) || bad_buffers(lse, k_len, ws) || bad_scale(scale)) return SVGEAR_ERR_INVALID_ARG;
     if (ws_bytes < svgear_cross_workspace_bytes(SVGEAR_CROSS_FORWARD, dims)) return SVGEAR_ERR_WORKSPACE;
     if (none) return SVGEAR_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -569,7 +569,8 @@ typedef enum {
 } svgear_cross_op;
 
 /* Workspace bytes of a cross attention call; 0 for arguments it would reject.
- * The workspace starts with the device status words (svgear_device_status). */
+ * The workspace is 16-byte aligned and starts with the device status words
+ * (svgear_device_status). */
 size_t svgear_cross_workspace_bytes(int32_t op, svgear_cross_dims dims);
 
 /* svgear_cross_attend -- softmax attention of every query over the keys

@@ -94,6 +94,19 @@ def test_backward_refusals(lib):
     assert call(dims=m.CrossDims(2, 4, 4, 100, 100, 80, m.BF16)) == m.ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("lse,k_len,ws", [(2, 0, 0), (0, 1, 0), (0, 2, 0), (0, 0, 4), (0, 0, 8)])
+def test_misaligned_buffers_are_refused(lib, lse, k_len, ws):
+    """Byte offsets of lse, k_len and the workspace that a load or store would fault on."""
+    m, t = lib, _tok(lib)
+    L, dims = m.lib(), m.CrossDims(2, 4, 4, 100, 100, 128, m.BF16)
+    lse, k_len, ws = FAKE + lse, FAKE + k_len if k_len else None, FAKE + ws
+    assert L.svgear_cross_attend(t, t, t, dims, k_len, 0.1, t, lse, ws, BIG, None) == m.ERR_INVALID_ARG
+    assert L.svgear_cross_attend_backward(t, t, t, t, t, lse, dims, k_len, 0.1, t, t, t, ws, BIG,
+                                          None) == m.ERR_INVALID_ARG
+    assert L.svgear_cross_attend_backward_ckpt(t, FAKE, FAKE, t, t, FAKE, FAKE, lse, dims, k_len, 0.1,
+                                               t, t, t, ws, BIG, None) == m.ERR_INVALID_ARG
+
+
 def test_checkpoint_refusals(lib):
     m = lib
     L, dims, t = m.lib(), m.Dims(2, 4, 100, 128, m.BF16), _tok(m)
