@@ -30,6 +30,10 @@ namespace {
 
 constexpr int kSimtMinTiles = 2;   // fewest 64-key tiles of a split
 
+// Queries or keys of a head: rounding up to a tile must not pass 32 bits (rows that
+// overlap, stride_n < d, make such lengths fit a GPU).
+constexpr int kMaxLength = INT32_MAX - 1023;
+
 int check_cross_dims(const svgear_cross_dims& d) {
     if (d.B < 0 || d.Hq < 0 || d.Hkv < 0 || d.Nq < 1 || d.Nk < 1) return SVGEAR_ERR_INVALID_ARG;
     if (d.dtype != SVGEAR_F32 && d.dtype != SVGEAR_BF16) return SVGEAR_ERR_UNSUPPORTED;
@@ -38,6 +42,7 @@ int check_cross_dims(const svgear_cross_dims& d) {
     if ((long long)d.B * d.Hq > 65535) return SVGEAR_ERR_UNSUPPORTED;   // grid y limit
     if ((long long)d.B * d.Hq * d.Nq >= (1ll << 31) || (long long)d.B * d.Hkv * d.Nk >= (1ll << 31))
         return SVGEAR_ERR_UNSUPPORTED;   // 32-bit row numbers
+    if (d.Nq > kMaxLength || d.Nk > kMaxLength) return SVGEAR_ERR_UNSUPPORTED;
     return SVGEAR_OK;
 }
 

@@ -555,7 +555,10 @@ typedef struct {
 
 /* Shapes of one call: Q, O and their gradients [B][Hq][Nq][d]; K, V and
  * theirs [B][Hkv][Nk][d].  Hkv divides Hq: query head h reads key/value head
- * h / (Hq / Hkv).  B, Hq >= 0 (0: nothing to do), Nq, Nk >= 1. */
+ * h / (Hq / Hkv).  B, Hq >= 0 (0: nothing to do), Nq, Nk >= 1.  At most 65,535
+ * (b, query head) pairs, fewer than 2^31 rows in a tensor and at most 2^31 - 1024
+ * in a head: else SVGEAR_ERR_UNSUPPORTED.  The checkpoint calls have the first two
+ * limits too. */
 typedef struct {
     int32_t B, Hq, Hkv, Nq, Nk, d;
     int32_t dtype; /* svgear_dtype */

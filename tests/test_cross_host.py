@@ -94,6 +94,17 @@ def test_backward_refusals(lib):
     assert call(dims=m.CrossDims(2, 4, 4, 100, 100, 80, m.BF16)) == m.ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("Nq,Nk", [(1, (1 << 31) - 1), (1, (1 << 31) - 1023), ((1 << 31) - 1, 1)])
+def test_lengths_whose_tiles_pass_32_bits_are_refused(lib, Nq, Nk):
+    m = lib
+    dims = m.CrossDims(1, 1, 1, Nq, Nk, 64, m.BF16)
+    t = _tok(m, N=1, H=1, d=64, sn=8)
+    assert m.lib().svgear_cross_workspace_bytes(m.CROSS_FORWARD, dims) == 0
+    assert _fwd(m, dims, t, t, t, t) == m.ERR_UNSUPPORTED
+    dims.Nq, dims.Nk = min(Nq, (1 << 31) - 1024), min(Nk, (1 << 31) - 1024)
+    assert m.lib().svgear_cross_workspace_bytes(m.CROSS_FORWARD, dims) > 0
+
+
 @pytest.mark.parametrize("lse,k_len,ws", [(2, 0, 0), (0, 1, 0), (0, 2, 0), (0, 0, 4), (0, 0, 8)])
 def test_misaligned_buffers_are_refused(lib, lse, k_len, ws):
     """Byte offsets of lse, k_len and the workspace that a load or store would fault on."""
