@@ -690,7 +690,9 @@ def svgear_cross_attend(Q, K, V, scale=None, k_len=None, O=None, lse=None, check
     default all; a batch with none gives 0 and lse -inf).  Tensors may be
     strided with d contiguous.  Returns (O, lse): O of Q's type and layout,
     lse float32 [B, Hq, Nq] for the backward pass.  scale defaults to
-    1 / sqrt(d)."""
+    1 / sqrt(d).  A given O or lse must not overlap an input.  As with every
+    call here torch records no gradient: svgear_cross_attend_backward gives
+    them."""
     q, k, v = _view(Q, "Q"), _view(K, "K", Q), _view(V, "V", Q, K.shape)
     dims = _cross_dims(Q.shape, K, k_len)
     if O is None:
@@ -773,7 +775,10 @@ def svgear_checkpoint_load(c, out=None):
 @_on_device("dO")
 def svgear_cross_attend_backward_ckpt(dO, Qc, K, V, Oc, lse, scale=None, k_len=None,
                                       check_status=False):
-    """svgear_cross_attend_backward with Q and O read from Checkpoints."""
+    """svgear_cross_attend_backward with Q and O read from Checkpoints.  The
+    gradients are those of the values the codes stand for, with the lse of the
+    Q that was saved: 1 % off the ones from the saved Q and O where the scores'
+    standard deviation is 1, 4 % where it is 4.5 (svgear.h)."""
     g = _view(dO, "dO")
     qc, qe = _held(Qc, "Qc", dO.shape, dO.device, dO.dtype)
     oc, oe = _held(Oc, "Oc", dO.shape, dO.device, dO.dtype)

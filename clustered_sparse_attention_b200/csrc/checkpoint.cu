@@ -3,8 +3,9 @@
 // |round(x / 2^e)| is at most 127, and each element is that rounded quotient
 // (half to even).  e stops at 121, where codes saturate at 127, so that a finite
 // value loads as a finite one.  The scaling by a power of two is exact, so the only
-// rounding is the one to the integer: |error| <= 2^(e-1), which is at most
-// 1/127 of the group's largest magnitude (2^e where codes saturate).
+// rounding is the one to the integer: |error| <= 2^(e-1), which for e > -127 is at most
+// 1/127 of the group's largest magnitude (2^e and 1/127 where codes saturate).  At
+// e = -127 it is the absolute 2^-128 alone: a group below that loads as zeros.
 //
 // Memory-bound: four units of 16 elements a thread (one 16-byte store of codes
 // each, one exponent byte per two threads).  75,600 x 40 x 128 bf16 saved and loaded in

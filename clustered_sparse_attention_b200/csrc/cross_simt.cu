@@ -89,7 +89,7 @@ __device__ __forceinline__ void dot_tile(const float* A, const float* Bm, int va
 // A product with a tile's weights is summed on its own and then added to the
 // running sum: n terms then take chains of 64 and n / 64 additions.  In one chain of
 // n the error of equal terms does not cancel (O over 75,600 equal keys: off by 9e-4,
-// now within 1e-5), and the additions saved are 1 in 64.
+// now by 2e-7, and the sum of the weights by 2e-5), and it saves one addition in 64.
 template <int C>
 __device__ __forceinline__ void clear(float (&x)[R][C]) {
 #pragma unroll

@@ -305,3 +305,27 @@ def test_tensor_memory_is_fenced_after_every_wait(name):
     # the scan sees the fault: without the first fence behind a wait
     at = text.index("fence_after_sync()", text.index("poll_bar("))
     assert unfenced_accesses(text[:at] + text[at + len("fence_after_sync()"):])
+
+
+def test_checkpoint_error_bound():
+    """|error| <= 2^(e-1), at most 1/127 of the group's largest magnitude for e > -127; 2^-128
+    at e = -127, where it may be all of a value; 2^e where codes saturate."""
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn(1, 1, 4000, 32, generator=g, dtype=torch.float64)
+    x = x * torch.exp2(torch.randint(-140, 126, (1, 1, 4000, 1), generator=g).double())
+    x[0, 0, 0] = torch.finfo(torch.float32).max
+    x[0, 0, 1] = 2.0 ** -130
+    x[0, 0, 2] = 0.4 * 2.0 ** -126
+    x = x.float().double()
+    codes, exps = co.pack(x)
+    e = exps[..., :1].double() - 127
+    err = (co.unpack(codes, exps) - x).abs().amax(-1, keepdim=True)
+    top = x.abs().amax(-1, keepdim=True)
+    assert bool((err <= torch.exp2(e - 1) + (e == 121) * torch.exp2(e - 1)).all())
+    low = e == -127
+    assert bool((err <= top / 127)[~low].all()) and bool((err[low] <= 2.0 ** -128).all())
+    assert bool(low[0, 0, 1:3].all()) and not codes[0, 0, 1].any()      # 2^-130: all of it lost
+    assert err[0, 0, 2] > 0.2 * top[0, 0, 2]
+    # exact in bf16 too: every loaded value is a bf16 number
+    y = co.unpack(codes, exps)
+    assert torch.equal(y.to(torch.bfloat16).double(), y)

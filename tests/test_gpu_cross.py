@@ -461,6 +461,39 @@ def test_backward_from_checkpoints(shape, dtype, d):
 
 
 @pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("gain", [1.0, 2.0])
+def test_checkpoint_gradients_beside_those_of_the_saved_tensors(dtype, gain):
+    """How far holding q and o in 8 bits moves the gradients, element by element: with
+    |q~ - q| <= h_q and |o~ - o| <= h_o (half a step of their groups),
+      |s~ - s| <= b = scale h_q.|k|,  |p~ - p| <= p (e^b - 1),  |D~ - D| <= c = |do|.h_o,
+      |ds~ - ds| <= w = p e^b c + p (e^b - 1) |do.v - D|,
+      |dq~ - dq| <= scale sum_j w |k|,  |dk~ - dk| <= scale sum_i (w |q~| + |ds| h_q),
+      |dv~ - dv| <= sum_i p (e^b - 1) |do|,
+    beside the bounds of the kernels' own arithmetic."""
+    csa, d, scale = _csa(), 64, 0.125
+    q, k, v, do = _inputs(44, 1, 2, 2, 130, 90, d, dtype, gain=gain)
+    O, lse = csa.svgear_cross_attend(q, k, v, scale)
+    qc, oc = csa.svgear_checkpoint_save(q), csa.svgear_checkpoint_save(O)
+    got = csa.svgear_cross_attend_backward_ckpt(do, qc, k, v, oc, lse, scale)
+    qh, oh = co.unpack(qc.codes, qc.exps), co.unpack(oc.codes, oc.exps)
+    _, tol = co.backward(do, qh, k, v, oh, lse, scale)
+    want, _ = co.backward(do, q, k, v, O, lse, scale)
+    q64, k64, v64, do64, o64, l64 = (t.cpu().double() for t in (q, k, v, do, O, lse))
+    hq, ho = (torch.exp2(c.exps.cpu().double() - 128).repeat_interleave(32, -1) for c in (qc, oc))
+    assert bool(((qh - q64).abs() <= hq).all()) and bool(((oh - o64).abs() <= ho).all())
+    p = torch.exp(scale * q64 @ k64.mT - l64[..., None])
+    g = do64 @ v64.mT - (do64 * o64).sum(-1, keepdim=True)
+    grow = torch.expm1(scale * hq @ k64.abs().mT)
+    c = (do64.abs() * ho).sum(-1, keepdim=True)
+    w = p * (1 + grow) * c + p * grow * g.abs()
+    moved = (scale * w @ k64.abs(),
+             scale * (w.mT @ qh.abs() + (p * g).abs().mT @ hq),
+             (p * grow).mT @ do64.abs())
+    for x, y, a, b, name in zip(got, want, tol, moved, ("dQ", "dK", "dV")):
+        _within(x, y, a + b, name)
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
 def test_checkpoints_captured_and_replayed(dtype):
     csa = _csa()
     q, k, v, do = _inputs(41, 2, 4, 2, 201, 140, 128, dtype)
