@@ -64,9 +64,10 @@ __device__ __forceinline__ float hi(uint64_t x) { return __uint_as_float((uint32
 // pipe idle, 3,300; now 2,980.)
 // TMEM: S | dP | dV | dK.
 // Bound: the chain S -> P -> dS -> dK between products that take 2,048 cycles of an
-// iteration, and at 75,600 x 512 keys, 40 heads, d = 128 (1.31-1.40 ms) the power
-// limit: its four products run at 1.2 PFLOP/s, 0.89 of a library product's sustained
-// rate.
+// iteration; in long runs also the power limit.  75,600 x 512 keys, 40 heads, d = 128:
+// 1.31-1.40 ms in runs of some 20 ms (1.2 PFLOP/s for its four products); the whole
+// pass, dQ and delta with it, 2.82 ms there and 3.33 at the power limit's clock (seven
+// products at 830 TFLOP/s, 0.61 of a library product's sustained rate).
 // A copy takes some 2,000 cycles to arrive.  Q(i) is held from S(i) to dK(i), so
 // its ring has three slots where dO's has two: with two of both, S(i + 1) waited
 // for its Q in every iteration (4,300 cycles each against 2,048 of MMA work).
@@ -451,7 +452,8 @@ cross_dkv_sm100_kernel(const __grid_constant__ KvMaps maps, CrossArgs a, float* 
 // its thread 100 to 300 cycles, a commit 65, and one thread for all three took
 // 3,400 cycles per tile for 1,536 of MMA work.  (With S in two buffers and dS over S, S(g + 2) came behind
 // dP(g + 1) and dQ(g) and the weights waited for it: some 3,000.)  Now 2,815 at
-// 75,600 x 512 keys, where an item ends every four tiles (1.16 ms, 40 heads, d = 128).
+// 75,600 x 512 keys, where an item ends every four tiles (1.16 ms in runs of some 20 ms,
+// 40 heads, d = 128).
 // Bound: the weights, which copy two 128 x 128 tiles from TMEM and one back between the
 // barriers of three products.
 // TMEM: S | dP[0] | dP[1] | dQ.

@@ -23,17 +23,18 @@
 //
 // Two accumulators of d columns, one per warpgroup, need no exchange between the
 // warpgroups within an item; 256 query rows per item sharing each key tile (half the
-// K and V copies) leave no TMEM for P beside S and took 875 us where this takes 797
-// (40 heads, 75,600 x 512 keys, d = 128).
+// K and V copies) leave no TMEM for P beside S and took 875 us where this took 797
+// (40 heads, 75,600 x 512 keys, d = 128, both in runs of some 20 ms).
 //
 // Bound: a tile costs some 2,100 cycles against 1,024 of MMA work (0.38-0.50 of the
 // tensor pipe): the two warpgroups' instructions for 128 x 128 weights and their copies
 // between TMEM and registers (about 350 cycles each beside running MMAs).  A quarter of
 // the exponentials as polynomials on the FMA pipe made it slower (836 us): the
-// length of each warp's chain counts, not the exponential unit.  1.0 PFLOP/s alone; 850 TFLOP/s when
-// repeated, the clock then falling to 1.5 GHz at the power limit.  Few rows over many
-// keys (77 x 118,800, 24 heads: 223 us) read K and V at 6.5 TB/s, the measured rate of a
-// copy.
+// length of each warp's chain counts, not the exponential unit.  820 us in the first 20 ms
+// of work (970 TFLOP/s); longer work reaches the power limit, the clock falls towards 1 GHz
+// and a call takes 965-975 us (820 TFLOP/s, 0.60 of a library product's sustained rate).
+// Few rows over many keys (77 x 118,800, 24 heads) read K and V at 6.2 TB/s at first
+// (235 us) and at 5.1-5.6 sustained (263-284 us), where a copy has 6.55.
 //
 // Every wait is bounded (tc_wait.cuh).
 #include <math.h>
