@@ -4,7 +4,10 @@
 //   dq_i = scale sum_j ds_ij k_j, dk_j = scale sum_i ds_ij q_i,
 //   dv_j = sum_i p_ij do_i.
 // p and ds enter their second product rounded to bf16 (an error of the size of
-// the outputs' own rounding); everything else, all sums among it, is fp32.
+// the outputs' own rounding); everything else, all sums among it, is fp32.  The
+// accumulators cut additions off (one for 16 rows), so equal terms come out low by
+// 3.3e-9 a term: 2.5e-4 for dK over 75,600 rows, a sixteenth of the output's rounding,
+// 2.1e-3 over 604,800 (a CTA adds no more rows than its share of the call).
 //
 // Two kernels, each recomputing the scores from Q and K: one keeps a key tile
 // and walks the queries (dK, dV), the other keeps a query tile and walks the
